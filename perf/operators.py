@@ -192,7 +192,7 @@ def _plain_scan(s):
     before = torch.cat([first, h[:, :-1]], 1)
     if s["reset"] is not None:
         before = torch.where(s["reset"][..., None], 0.0, before)
-    dout = s["dout"].float()
+    dout = s["dout"].to(torch.float32, copy=True)  # the state's own dout stays as it is
     dout[:, -1] += s["dstate"]
     # the reverse recurrence g_t = dout_t + held_{t+1} g_{t+1}, as a forward one over the flipped tokens
     after = torch.cat([held[:, 1:], torch.zeros_like(held[:, :1])], 1)
