@@ -82,7 +82,9 @@ enum {
     FALCON_OK = 0,
     FALCON_ERR_NULL = -1,        /* a required pointer is NULL                      */
     FALCON_ERR_ENUM = -2,        /* variant / form / dtype / pairing / phi invalid   */
-    FALCON_ERR_SHAPE = -3,       /* B,H,L < 0, or d_k, d_v not in {16,32,64,128}     */
+    FALCON_ERR_SHAPE = -3,       /* B,H,L < 0, or d_k, d_v not in {16,32,64,128}; the
+                                    layer operators: a size or row stride out of its
+                                    range                                          */
     FALCON_ERR_CHUNK = -4,       /* chunk not in {16,32,64} (or 128 where taken)     */
     FALCON_ERR_WINDOW = -6,      /* window < 1 or > 8 for Falcon-3/3A               */
     FALCON_ERR_LAUNCH = -7,      /* a kernel launch failed (cudaGetLastError)       */
@@ -417,6 +419,160 @@ int falcon_decode_carry_from_prefill_ex(falcon_variant variant, falcon_dtype dty
                                         const void *k, const void *v, int window,
                                         int B, int H, int L, int d_k, int d_v,
                                         float *x_prev, float *win, cudaStream_t stream);
+
+/*
+ * The operators of the layer around the update: a gated linear recurrence
+ * (the sibling of the matrix state with one state per channel, for the
+ * layers of a stack that keep that little), the gated norm behind a block
+ * and the residual norm in front of one.  For all of them:
+ *  - activations and their gradients are `dtype`; states, marks, weights and
+ *    the weights' gradients are fp32; sums, states and norms are held in
+ *    fp32 and rounded once, when they are stored;
+ *  - results do not depend on the launch: every sum has a fixed order, so
+ *    the same call on the same device gives the same bits;
+ *  - the last axis is contiguous; where a row stride is an argument it counts
+ *    elements from one token to the next and is at least the row's length
+ *    (FALCON_ERR_SHAPE otherwise), so the halves of one projection are read
+ *    (and their gradients written) in place;
+ *  - outputs must not overlap inputs unless said otherwise;
+ *  - nothing is allocated: the backward passes run in the caller's workspace
+ *    (256-byte aligned, at least the bytes of the size query for the same
+ *    sizes; FALCON_ERR_WORKSPACE otherwise), which two calls may share only
+ *    if they cannot overlap on the GPU (captured graphs included);
+ *  - a size of zero is no error: outputs of no elements are left alone, a
+ *    final state of no tokens is the initial one, a weight's gradient over no
+ *    rows is zero.
+ */
+
+/* Tokens between two marks of falcon_scan. */
+#define FALCON_SCAN_BLOCK 128
+/* The longest row of the norms. */
+#define FALCON_NORM_MAX_D 16384
+
+/*
+ * falcon_scan -- the gated linear recurrence over N sequences of L tokens and
+ * D channels, each channel by itself:
+ *   a_t = 1 / (1 + exp(-f_t))
+ *   h_t = (reset_t ? 0 : a_t h_{t-1}) + (1 - a_t) x_t,   out_t = h_t
+ *
+ *   x, f     [N,L,D] dtype, row strides x_stride and f_stride (sequence n
+ *            begins at n*L*stride): values and forget gates.  f = +inf keeps
+ *            the state as it is (x finite), f = -inf replaces it.
+ *   reset    [N,L] bytes, or NULL: where non-zero, token t begins a new
+ *            document in a packed sequence and what came before does not
+ *            reach it, whatever its value (infinities and NaN included)
+ *   initial_state [N,D] fp32, or NULL (zeros): h before the first token
+ *   out      [N,L,D] dtype, contiguous, written
+ *   final_state   [N,D] fp32, written, or NULL; may be initial_state
+ *   marks    [N,ceil(L/FALCON_SCAN_BLOCK),D] fp32, written, or NULL: the state
+ *            entering every block of FALCON_SCAN_BLOCK tokens, which
+ *            falcon_scan_bwd_ws continues from
+ */
+int falcon_scan(falcon_dtype dtype, const void *x, const void *f, const unsigned char *reset,
+                const float *initial_state, int N, int L, int D, long long x_stride, long long f_stride,
+                void *out, float *final_state, float *marks, cudaStream_t stream);
+
+/*
+ * falcon_scan_bwd_ws -- its backward pass: given dout = dL/d(out) and dstate
+ * = dL/d(final_state),
+ *   g_t  = dout_t + (reset_{t+1} ? 0 : a_{t+1} g_{t+1}),   g_L = dout_L + dstate
+ *   dx_t = (1 - a_t) g_t
+ *   df_t = a_t (1 - a_t) g_t ((reset_t ? 0 : h_{t-1}) - x_t)
+ *   dinitial = reset_1 ? 0 : a_1 g_1
+ *
+ *   marks    as falcon_scan wrote them for the same x, f, reset and initial
+ *            state, or NULL: they are formed again first, in the workspace
+ *            (with marks the workspace is not used)
+ *   dout     [N,L,D] dtype, contiguous;  dstate [N,D] fp32, or NULL (zero)
+ *   dx, df   [N,L,D] dtype, row strides dx_stride and df_stride, written
+ *   dinitial [N,D] fp32, written, or NULL
+ */
+int falcon_scan_bwd_workspace_size(falcon_dtype dtype, int N, int L, int D, int has_marks, size_t *bytes);
+int falcon_scan_bwd_ws(falcon_dtype dtype, const void *x, const void *f, const unsigned char *reset,
+                       const float *initial_state, const float *marks, int N, int L, int D, long long x_stride,
+                       long long f_stride, const void *dout, const float *dstate, void *dx, long long dx_stride,
+                       void *df, long long df_stride, float *dinitial, void *workspace, size_t workspace_bytes,
+                       cudaStream_t stream);
+
+/*
+ * falcon_scan_step -- one token of N sequences (decode): x, f [N,D] with row
+ * strides, state [N,D] fp32 read, state_out [N,D] fp32 written (may be
+ * `state`), out [N,D] dtype, contiguous, written.
+ */
+int falcon_scan_step(falcon_dtype dtype, const void *x, const void *f, const float *state, int N, int D,
+                     long long x_stride, long long f_stride, float *state_out, void *out, cudaStream_t stream);
+
+/*
+ * falcon_norm_gate -- the norm behind a block, with its gate, from the layout
+ * falcon_fwd writes to the one the output projection reads:
+ *   n = o / sqrt(mean_c(o^2) + eps)          over the d channels of a head
+ *   out[b,l,h*d+c] = n[c] * weight[c] * s(gate[b,l,h*d+c]),
+ *   s(z) = z / (1 + exp(-z))
+ *
+ *   o        element (b,h,l,c) at b*o_sb + h*o_sh + l*o_sl + c, dtype
+ *            (falcon_fwd's out: o_sl = d, o_sh = L*d, o_sb = H*L*d)
+ *   gate     [B,L,H*d] dtype, row stride gate_stride (token (b,l) is row
+ *            b*L+l), or NULL: no gate
+ *   weight   [d] fp32, or [H,d] with per_head != 0, or NULL: ones
+ *   eps      >= 0 (FALCON_ERR_UNSUPPORTED otherwise); a row of zeros with
+ *            eps = 0 gives zeros
+ *   d        1..FALCON_NORM_MAX_D
+ *   out      [B,L,H*d] dtype, contiguous, written
+ */
+int falcon_norm_gate(falcon_dtype dtype, const void *o, long long o_sb, long long o_sh, long long o_sl,
+                     const void *gate, long long gate_stride, const float *weight, int per_head, float eps,
+                     int B, int H, int L, int d, void *out, cudaStream_t stream);
+
+/*
+ * falcon_norm_gate_bwd_ws -- its backward pass, with e = dout s(gate), r = 1 /
+ * sqrt(mean(o^2) + eps):
+ *   d_o     = r (e w - n mean_c(e w n))   at d_o_sb, d_o_sh, d_o_sl, written
+ *   dgate   = dout n w s'(gate)           [B,L,H*d], row stride dgate_stride,
+ *             written; NULL exactly when gate is (FALCON_ERR_NULL otherwise)
+ *   dweight = sum over the tokens (and, for a shared weight, the heads) of
+ *             e n                         fp32, written, or NULL
+ */
+int falcon_norm_gate_bwd_workspace_size(falcon_dtype dtype, int B, int H, int L, int d, size_t *bytes);
+int falcon_norm_gate_bwd_ws(falcon_dtype dtype, const void *o, long long o_sb, long long o_sh, long long o_sl,
+                            const void *gate, long long gate_stride, const float *weight, int per_head, float eps,
+                            int B, int H, int L, int d, const void *dout, void *d_o, long long d_o_sb,
+                            long long d_o_sh, long long d_o_sl, void *dgate, long long dgate_stride, float *dweight,
+                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * falcon_residual_norm -- the norm in front of a block, with the residual
+ * add and the scale of what is added, over R rows of D channels:
+ *   r_out = r + scale * y
+ *   h     = r_out / sqrt(mean(r_out^2) + eps) * weight
+ * h is formed from r_out before r_out is rounded.
+ *
+ *   r, y     [R,D] dtype, contiguous; y may be NULL (r_out = r)
+ *   scale    [D] fp32, or NULL: ones
+ *   weight   [D] fp32, or NULL: ones;  eps as in falcon_norm_gate
+ *   D        1..FALCON_NORM_MAX_D
+ *   r_out    [R,D] dtype, written, or NULL; may be r or y
+ *   h        [R,D] dtype, written; may be r or y, not r_out
+ */
+int falcon_residual_norm(falcon_dtype dtype, const void *r, const void *y, const float *scale, const float *weight,
+                         float eps, int R, int D, void *r_out, void *h, cudaStream_t stream);
+
+/*
+ * falcon_residual_norm_bwd_ws -- its backward pass from r_out as the forward
+ * left it, given dh = dL/dh and dr_out = dL/d(r_out) from what reads the
+ * stream further on (NULL: zero).  With n = r_out / sqrt(mean(r_out^2) + eps),
+ * rstd that quotient's factor and e = dh weight:
+ *   dr      = dr_out + rstd (e - n mean(e n))   written
+ *   dy      = scale * dr (before dr is rounded) written; may be NULL (with
+ *             scale NULL it would be dr)
+ *   dscale  = sum over the rows of dr * y   fp32, written, or NULL (needs y)
+ *   dweight = sum over the rows of dh * n   fp32, written, or NULL
+ * dr may be dr_out or dh; dy may be y.
+ */
+int falcon_residual_norm_bwd_workspace_size(falcon_dtype dtype, int R, int D, size_t *bytes);
+int falcon_residual_norm_bwd_ws(falcon_dtype dtype, const void *r_out, const void *y, const float *scale,
+                                const float *weight, const void *dh, const void *dr_out, float eps, int R, int D,
+                                void *dr, void *dy, float *dscale, float *dweight, void *workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * falcon_fwd_masked_noalloc -- the masked-parallel forward (prefix pair, L2

@@ -26,7 +26,10 @@ EXPORTS = ("falcon_fwd", "falcon_fwd_ex", "falcon_fwd_workspace_size", "falcon_f
            "falcon_bwd", "falcon_bwd_ex", "falcon_bwd_workspace_size", "falcon_bwd_ws", "falcon_decode_step",
            "falcon_decode_step_ex", "falcon_decode_carry_from_prefill", "falcon_decode_carry_from_prefill_ex",
            "falcon_fwd_masked_noalloc", "falcon_device_wait_timeouts", "falcon_selftest_bounded_wait",
-           "falcon_scratch_trim", "falcon_status_string")
+           "falcon_scratch_trim", "falcon_status_string", "falcon_scan", "falcon_scan_bwd_workspace_size",
+           "falcon_scan_bwd_ws", "falcon_scan_step", "falcon_norm_gate", "falcon_norm_gate_bwd_workspace_size",
+           "falcon_norm_gate_bwd_ws", "falcon_residual_norm", "falcon_residual_norm_bwd_workspace_size",
+           "falcon_residual_norm_bwd_ws")
 
 _lib = None
 
@@ -89,6 +92,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.falcon_scratch_trim.restype = I
     lib.falcon_status_string.argtypes = [I]
     lib.falcon_status_string.restype = ctypes.c_char_p
+    W = ctypes.c_longlong
+    layer = {
+        "falcon_scan": [I, P, P, P, P, I, I, I, W, W, P, P, P, P],
+        "falcon_scan_bwd_workspace_size": [I, I, I, I, I, ZP],
+        "falcon_scan_bwd_ws": [I, P, P, P, P, P, I, I, I, W, W, P, P, P, W, P, W, P, P, Z, P],
+        "falcon_scan_step": [I, P, P, P, I, I, W, W, P, P, P],
+        "falcon_norm_gate": [I, P, W, W, W, P, W, P, I, F, I, I, I, I, P, P],
+        "falcon_norm_gate_bwd_workspace_size": [I, I, I, I, I, ZP],
+        "falcon_norm_gate_bwd_ws": [I, P, W, W, W, P, W, P, I, F, I, I, I, I, P, P, W, W, W, P, W, P, P, Z, P],
+        "falcon_residual_norm": [I, P, P, P, P, F, I, I, P, P, P],
+        "falcon_residual_norm_bwd_workspace_size": [I, I, I, ZP],
+        "falcon_residual_norm_bwd_ws": [I, P, P, P, P, P, P, F, I, I, P, P, P, P, P, Z, P],
+    }
+    for name, argtypes in layer.items():
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = argtypes, I
     _lib = lib
     return lib
 

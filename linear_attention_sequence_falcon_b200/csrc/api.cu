@@ -393,7 +393,9 @@ extern "C" const char *falcon_status_string(int status) {
         case FALCON_OK: return "ok";
         case FALCON_ERR_NULL: return "a required pointer is NULL";
         case FALCON_ERR_ENUM: return "invalid variant, form, dtype, pairing or feature map";
-        case FALCON_ERR_SHAPE: return "unsupported shape: B,H,L must be >= 0 and d_k,d_v in {16,32,64,128}";
+        case FALCON_ERR_SHAPE:
+            return "unsupported shape: B,H,L must be >= 0 and d_k,d_v in {16,32,64,128} (the layer operators: sizes "
+                   "and row strides in their ranges)";
         case FALCON_ERR_CHUNK:
             return "chunk must be 16, 32 or 64 for the chunk-parallel form (128: Falcon-1/1A, bf16, d = 32 or 64)";
         case FALCON_ERR_WINDOW: return "window must be in [1,8] for Falcon-3/3A";

@@ -1,0 +1,403 @@
+"""The operators of the layer around a Falcon update, bound from libfalcon.so:
+the gated linear recurrence (scan, scan_bwd, scan_step), the gated norm behind
+a block (norm_gate, norm_gate_bwd) and the residual norm in front of one
+(residual_norm, residual_norm_bwd).
+
+Activations and their gradients share one dtype, fp32 or bf16; states, marks,
+weights and the weights' gradients are fp32.  Every array is checked before a
+pointer reaches the library (FalconError).  Calls enqueue on torch's current
+stream of the tensors' device, or on the stream given (outputs and workspaces
+made here then belong to that stream), and return without synchronising; work
+that made the inputs on another stream is the caller's to wait for.  Rows are
+read through a row stride where the arguments say "rows": [.., L, D] with a
+contiguous last axis whose tokens lie evenly, such as half of a projection.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from ._lib import DTYPES, FalconError, _check, _shape_error, load
+
+SCAN_BLOCK = 128     # tokens between two marks of scan
+NORM_MAX_D = 16384   # the longest row of the norms
+
+
+def _on(device, stream):
+    """Makes `device` current, and `stream` with it, for one call."""
+    if device.type != "cuda":
+        raise FalconError("tensor is not on a CUDA device (no CPU path exists)")
+    if stream is not None:
+        if stream.device != device:
+            raise FalconError("the stream is on %s, the tensors on %s" % (stream.device, device))
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _need(t, name, shape, dtype, device):
+    """A contiguous array of this shape, dtype and device (or None)."""
+    if t is None:
+        return
+    if tuple(t.shape) != shape:
+        _shape_error("%s must be %s, got %s" % (name, shape, tuple(t.shape)))
+    if t.dtype != dtype:
+        raise FalconError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise FalconError("%s is on %s, not on %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        raise FalconError("%s must be contiguous" % name)
+
+
+def _rows(t, name, shape, dtype, device):
+    """The row stride of an array of rows: contiguous last axis, the tokens of
+    all its sequences evenly spaced."""
+    if tuple(t.shape) != shape:
+        _shape_error("%s must be %s, got %s" % (name, shape, tuple(t.shape)))
+    if t.dtype != dtype:
+        raise FalconError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise FalconError("%s is on %s, not on %s" % (name, t.device, device))
+    D = shape[-1]
+    if t.is_contiguous():
+        return D
+    st = t.stride()
+    if D > 1 and st[-1] != 1:
+        raise FalconError("the last axis of %s must be contiguous" % name)
+    step, span = None, 1  # tokens covered by the axes seen so far, from the last one outwards
+    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step = s
+        elif s != step * span:
+            raise FalconError("the rows of %s must be evenly spaced (strides %s)" % (name, st))
+        span *= n
+    if step is not None and step < D:
+        raise FalconError("the rows of %s overlap (strides %s)" % (name, st))
+    return D if step is None else step
+
+
+def _apart(t, name):
+    """Refuses an array to be written whose elements share memory."""
+    span = 1
+    for s, n in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
+        if s < span:
+            raise FalconError("the elements of %s overlap (strides %s)" % (name, t.stride()))
+        span = s * n
+
+
+def _dtype(t, name):
+    if t.dtype not in DTYPES:
+        raise FalconError("%s must be fp32 or bf16, got %s" % (name, t.dtype))
+    return DTYPES[t.dtype]
+
+
+def _workspace(need, workspace, device):
+    if need == 0:
+        return None, 0
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if workspace.device != device or not workspace.is_contiguous():
+        raise FalconError("workspace must be a contiguous array on %s" % (device,))
+    have = workspace.numel() * workspace.element_size()
+    if have < need:
+        raise FalconError("workspace of %d bytes is smaller than the %d the call needs" % (have, need))
+    return workspace, have
+
+
+def _eps(eps):
+    eps = float(eps)
+    if not eps >= 0.0:
+        raise FalconError("eps must be >= 0, got %r" % eps)
+    return eps
+
+
+# ---------------------------------------------------------------- the gated linear recurrence
+
+def check_scan_shapes(x, f, reset=None, initial_state=None, out=None, final_state=None, marks=None, dout=None,
+                      dstate=None, dx=None, df=None):
+    """Checks the arrays of scan and scan_bwd against x's [N,L,D]: f like x,
+    reset [N,L] bool or uint8, states [N,D] fp32, marks
+    [N,ceil(L/SCAN_BLOCK),D] fp32; x, f, dx, df are rows, the others
+    contiguous.  Returns (N, L, D, row stride of x, row stride of f)."""
+    if x.dim() != 3:
+        _shape_error("x must be [N,L,D], got %s" % (tuple(x.shape),))
+    _dtype(x, "x")
+    shape = N, L, D = tuple(x.shape)
+    dev = x.device
+    ldx = _rows(x, "x", shape, x.dtype, dev)
+    ldf = _rows(f, "f", shape, x.dtype, dev)
+    if reset is not None:
+        if reset.dtype not in (torch.bool, torch.uint8):
+            raise FalconError("reset must be bool or uint8, got %s" % reset.dtype)
+        _need(reset, "reset", (N, L), reset.dtype, dev)
+    for t, name in ((initial_state, "initial_state"), (final_state, "final_state"), (dstate, "dstate")):
+        _need(t, name, (N, D), torch.float32, dev)
+    _need(marks, "marks", (N, -(-L // SCAN_BLOCK), D), torch.float32, dev)
+    _need(out, "out", shape, x.dtype, dev)
+    _need(dout, "dout", shape, x.dtype, dev)
+    for t, name in ((dx, "dx"), (df, "df")):
+        if t is not None:
+            _rows(t, name, shape, x.dtype, dev)
+    return N, L, D, ldx, ldf
+
+
+def scan(x, f, reset=None, initial_state=None, out=None, final_state=None, marks=None, want_state=True,
+         want_marks=False, stream=None):
+    """falcon_scan: h_t = sigmoid(f_t) h_{t-1} + (1 - sigmoid(f_t)) x_t for each
+    of the D channels of N sequences, x and f [N,L,D] (rows).  Where reset
+    [N,L] is set, what came before the token does not reach it (documents
+    packed into one sequence).  Returns (out, final_state), and with
+    want_marks the marks that scan_bwd continues from: (out, final_state,
+    marks)."""
+    lib = load()
+    N, L, D, ldx, ldf = check_scan_shapes(x, f, reset, initial_state, out, final_state, marks)
+    with _on(x.device, stream):
+        if out is None:
+            out = torch.empty((N, L, D), dtype=x.dtype, device=x.device)
+        if final_state is None and want_state:
+            final_state = torch.empty((N, D), dtype=torch.float32, device=x.device)
+        if marks is None and want_marks:
+            marks = torch.empty((N, -(-L // SCAN_BLOCK), D), dtype=torch.float32, device=x.device)
+        _check(lib.falcon_scan(DTYPES[x.dtype], _p(x), _p(f), _p(reset), _p(initial_state), N, L, D, ldx, ldf,
+                               _p(out), _p(final_state), _p(marks), _raw_stream()))
+    return (out, final_state, marks) if want_marks else (out, final_state)
+
+
+def scan_bwd_workspace_size(dtype, N: int, L: int, D: int, has_marks: bool) -> int:
+    """falcon_scan_bwd_workspace_size: device bytes of scan_bwd's workspace."""
+    n = ctypes.c_size_t(0)
+    _check(load().falcon_scan_bwd_workspace_size(DTYPES[dtype], N, L, D, int(has_marks), ctypes.byref(n)))
+    return int(n.value)
+
+
+def scan_bwd(x, f, dout, dstate=None, reset=None, initial_state=None, marks=None, dx=None, df=None, stream=None,
+             workspace=None):
+    """falcon_scan_bwd_ws: the gradients of scan given dout [N,L,D] and dstate
+    [N,D] fp32 (None: zero).  `marks` are those of scan with the same x, f,
+    reset and initial_state; without them they are formed again first.
+    Returns a dict: dx, df [N,L,D] (written into `dx`, `df` where given: rows)
+    and dinitial [N,D] fp32."""
+    lib = load()
+    N, L, D, ldx, ldf = check_scan_shapes(x, f, reset, initial_state, None, None, marks, dout, dstate, dx, df)
+    with _on(x.device, stream):
+        if dx is None:
+            dx = torch.empty((N, L, D), dtype=x.dtype, device=x.device)
+        if df is None:
+            df = torch.empty((N, L, D), dtype=x.dtype, device=x.device)
+        dinitial = torch.empty((N, D), dtype=torch.float32, device=x.device)
+        need = 0 if marks is not None else scan_bwd_workspace_size(x.dtype, N, L, D, False)
+        ws, have = _workspace(need, workspace, x.device)
+        _check(lib.falcon_scan_bwd_ws(DTYPES[x.dtype], _p(x), _p(f), _p(reset), _p(initial_state), _p(marks), N, L,
+                                      D, ldx, ldf, _p(dout), _p(dstate), _p(dx),
+                                      _rows(dx, "dx", (N, L, D), x.dtype, x.device), _p(df),
+                                      _rows(df, "df", (N, L, D), x.dtype, x.device), _p(dinitial), _p(ws), have,
+                                      _raw_stream()))
+    return {"dx": dx, "df": df, "dinitial": dinitial}
+
+
+def scan_step(x, f, state, state_out=None, out=None, stream=None):
+    """falcon_scan_step: one token of N sequences, x and f [N,D] (rows), state
+    [N,D] fp32.  The new state is written to state_out, or over `state`
+    without one.  Returns (out [N,D], the new state)."""
+    lib = load()
+    if x.dim() != 2:
+        _shape_error("x must be [N,D], got %s" % (tuple(x.shape),))
+    dt = _dtype(x, "x")
+    shape = N, D = tuple(x.shape)
+    dev = x.device
+    ldx = _rows(x, "x", shape, x.dtype, dev)
+    ldf = _rows(f, "f", shape, x.dtype, dev)
+    if state_out is None:
+        state_out = state
+    _need(state, "state", shape, torch.float32, dev)
+    _need(state_out, "state_out", shape, torch.float32, dev)
+    _need(out, "out", shape, x.dtype, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=x.dtype, device=dev)
+        _check(lib.falcon_scan_step(dt, _p(x), _p(f), _p(state), N, D, ldx, ldf, _p(state_out), _p(out),
+                                    _raw_stream()))
+    return out, state_out
+
+
+# ---------------------------------------------------------------- the gated norm behind a block
+
+def check_norm_gate_shapes(o, gate, weight, out=None, dout=None, do=None, dgate=None):
+    """Checks the arrays of norm_gate and norm_gate_bwd against o's [B,H,L,d]
+    (any strides, contiguous last axis): gate and dgate [B,L,H*d] (rows) or
+    None, weight [d] or [H,d] fp32 or None, out and dout [B,L,H*d] contiguous,
+    do like o.  Returns (B, H, L, d, row stride of gate)."""
+    if o.dim() != 4:
+        _shape_error("o must be [B,H,L,d], got %s" % (tuple(o.shape),))
+    _dtype(o, "o")
+    B, H, L, d = o.shape
+    if not 1 <= d <= NORM_MAX_D:
+        _shape_error("the rows must have 1 to %d channels, got %d" % (NORM_MAX_D, d))
+    dev = o.device
+    for t, name in ((o, "o"), (do, "do")):
+        if t is not None and d > 1 and t.stride(-1) != 1:
+            raise FalconError("the last axis of %s must be contiguous" % name)
+    if do is not None and (tuple(do.shape) != (B, H, L, d) or do.dtype != o.dtype or do.device != dev):
+        _shape_error("do must be like o")
+    if do is not None:
+        _apart(do, "do")
+    ldg = H * d
+    if gate is not None:
+        ldg = _rows(gate, "gate", (B, L, H * d), o.dtype, dev)
+    if dgate is not None:
+        _rows(dgate, "dgate", (B, L, H * d), o.dtype, dev)
+    if weight is not None and weight.dim() == 1:
+        _need(weight, "weight", (d,), torch.float32, dev)
+    else:
+        _need(weight, "weight", (H, d), torch.float32, dev)
+    _need(out, "out", (B, L, H * d), o.dtype, dev)
+    _need(dout, "dout", (B, L, H * d), o.dtype, dev)
+    return B, H, L, d, ldg
+
+
+def norm_gate(o, gate, weight, eps: float, out=None, stream=None):
+    """falcon_norm_gate: o [B,H,L,d] (what fwd returns, or any strides)
+    divided by each row's root mean square, times weight ([d], or [H,d] for
+    one per head; None: ones) and z/(1+exp(-z)) of gate [B,L,H*d] (rows; None:
+    no gate).  Returns [B,L,H*d], the layout of the output projection."""
+    lib = load()
+    B, H, L, d, ldg = check_norm_gate_shapes(o, gate, weight, out)
+    eps = _eps(eps)
+    with _on(o.device, stream):
+        if out is None:
+            out = torch.empty((B, L, H * d), dtype=o.dtype, device=o.device)
+        sb, sh, sl, _ = o.stride()
+        _check(lib.falcon_norm_gate(DTYPES[o.dtype], _p(o), sb, sh, sl, _p(gate), ldg, _p(weight),
+                                    int(weight is not None and weight.dim() == 2), eps, B, H, L, d, _p(out),
+                                    _raw_stream()))
+    return out
+
+
+def norm_gate_bwd_workspace_size(dtype, B: int, H: int, L: int, d: int) -> int:
+    """falcon_norm_gate_bwd_workspace_size: device bytes of norm_gate_bwd's workspace."""
+    n = ctypes.c_size_t(0)
+    _check(load().falcon_norm_gate_bwd_workspace_size(DTYPES[dtype], B, H, L, d, ctypes.byref(n)))
+    return int(n.value)
+
+
+def norm_gate_bwd(o, gate, weight, eps: float, dout, do=None, dgate=None, want_dweight=True, stream=None,
+                  workspace=None):
+    """falcon_norm_gate_bwd_ws: the gradients of norm_gate given dout
+    [B,L,H*d].  Returns a dict: do [B,H,L,d] (contiguous, as bwd takes its
+    dout, or written into `do` with its strides), dgate [B,L,H*d] (rows where
+    given; None without a gate), dweight fp32 like weight (None without one,
+    or with want_dweight=False)."""
+    lib = load()
+    B, H, L, d, ldg = check_norm_gate_shapes(o, gate, weight, None, dout, do, dgate)
+    if gate is None and dgate is not None:
+        raise FalconError("dgate without a gate")
+    eps = _eps(eps)
+    with _on(o.device, stream):
+        if do is None:
+            do = torch.empty((B, H, L, d), dtype=o.dtype, device=o.device)
+        if dgate is None and gate is not None:
+            dgate = torch.empty((B, L, H * d), dtype=o.dtype, device=o.device)
+        lddg = H * d if dgate is None else _rows(dgate, "dgate", (B, L, H * d), o.dtype, o.device)
+        dweight = torch.empty_like(weight) if weight is not None and want_dweight else None
+        ws, have = _workspace(norm_gate_bwd_workspace_size(o.dtype, B, H, L, d), workspace, o.device)
+        sb, sh, sl, _ = o.stride()
+        tb, th, tl, _ = do.stride()
+        _check(lib.falcon_norm_gate_bwd_ws(DTYPES[o.dtype], _p(o), sb, sh, sl, _p(gate), ldg, _p(weight),
+                                           int(weight is not None and weight.dim() == 2), eps, B, H, L, d, _p(dout),
+                                           _p(do), tb, th, tl, _p(dgate), lddg, _p(dweight), _p(ws), have,
+                                           _raw_stream()))
+    return {"do": do, "dgate": dgate, "dweight": dweight}
+
+
+# ---------------------------------------------------------------- the residual norm in front of a block
+
+def check_residual_norm_shapes(r, weight, y=None, scale=None, **like_r):
+    """Checks the arrays of residual_norm and residual_norm_bwd against r's
+    [..., D]: y and every other activation like r and contiguous, scale and
+    weight [D] fp32 or None.  Returns (rows, D)."""
+    if r.dim() < 1:
+        _shape_error("r must be [..., D]")
+    _dtype(r, "r")
+    shape, dev = tuple(r.shape), r.device
+    D = shape[-1]
+    if not 1 <= D <= NORM_MAX_D:
+        _shape_error("the rows must have 1 to %d channels, got %d" % (NORM_MAX_D, D))
+    _need(r, "r", shape, r.dtype, dev)
+    _need(y, "y", shape, r.dtype, dev)
+    for name, t in like_r.items():
+        _need(t, name, shape, r.dtype, dev)
+    _need(scale, "scale", (D,), torch.float32, dev)
+    _need(weight, "weight", (D,), torch.float32, dev)
+    if scale is not None and y is None:
+        raise FalconError("a scale without what it scales (y)")
+    return r.numel() // D, D
+
+
+def residual_norm(r, weight, eps: float, y=None, scale=None, r_out=None, h=None, stream=None):
+    """falcon_residual_norm: the residual stream r [..., D] plus scale [D] times
+    y, and that divided by its root mean square, times weight [D].  Returns
+    (r_out, h); r_out may be `r` itself (the stream updated in place), and is
+    `r` where there is no y."""
+    lib = load()
+    R, D = check_residual_norm_shapes(r, weight, y, scale, r_out=r_out, h=h)
+    eps = _eps(eps)
+    if h is not None and r_out is not None and h.data_ptr() == r_out.data_ptr() and R:
+        raise FalconError("h and r_out are the same array")
+    with _on(r.device, stream):
+        if h is None:
+            h = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+        write = r_out
+        if y is not None and r_out is None:
+            write = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+        _check(lib.falcon_residual_norm(DTYPES[r.dtype], _p(r), _p(y), _p(scale), _p(weight), eps, R, D, _p(write),
+                                        _p(h), _raw_stream()))
+    return (r if write is None else write), h
+
+
+def residual_norm_bwd_workspace_size(dtype, R: int, D: int) -> int:
+    """falcon_residual_norm_bwd_workspace_size: device bytes of residual_norm_bwd's workspace."""
+    n = ctypes.c_size_t(0)
+    _check(load().falcon_residual_norm_bwd_workspace_size(DTYPES[dtype], R, D, ctypes.byref(n)))
+    return int(n.value)
+
+
+def residual_norm_bwd(r_out, weight, eps: float, dh, dr_out=None, y=None, scale=None, dr=None, dy=None, stream=None,
+                      workspace=None):
+    """falcon_residual_norm_bwd_ws: the gradients of residual_norm from r_out as
+    it returned it, given dh and dr_out (the gradient of r_out from what else
+    reads the stream; None: zero).  Returns a dict: dr (of r), dy (of y; the
+    same tensor as dr without a scale; None without y), dscale, dweight fp32
+    (None without scale, weight).  dr may be dr_out or dh."""
+    lib = load()
+    R, D = check_residual_norm_shapes(r_out, weight, y, scale, dh=dh, dr_out=dr_out, dr=dr, dy=dy)
+    eps = _eps(eps)
+    if dy is not None and scale is None:
+        raise FalconError("without a scale dy is dr: it is not written apart")
+    if dr is not None and dy is not None and dr.data_ptr() == dy.data_ptr() and R:
+        raise FalconError("dr and dy are the same array")
+    with _on(r_out.device, stream):
+        if dr is None:
+            dr = torch.empty(r_out.shape, dtype=r_out.dtype, device=r_out.device)
+        if dy is None and scale is not None:
+            dy = torch.empty(r_out.shape, dtype=r_out.dtype, device=r_out.device)
+        dscale = None if scale is None else torch.empty_like(scale)
+        dweight = None if weight is None else torch.empty_like(weight)
+        ws, have = _workspace(residual_norm_bwd_workspace_size(r_out.dtype, R, D), workspace, r_out.device)
+        _check(lib.falcon_residual_norm_bwd_ws(DTYPES[r_out.dtype], _p(r_out), _p(y), _p(scale), _p(weight), _p(dh),
+                                               _p(dr_out), eps, R, D, _p(dr), _p(dy), _p(dscale), _p(dweight),
+                                               _p(ws), have, _raw_stream()))
+    return {"dr": dr, "dy": dy if scale is not None else (dr if y is not None else None), "dscale": dscale,
+            "dweight": dweight}
