@@ -445,7 +445,7 @@ int falcon_decode_carry_from_prefill_ex(falcon_variant variant, falcon_dtype dty
  */
 
 /* Tokens between two marks of falcon_scan. */
-#define FALCON_SCAN_BLOCK 128
+#define FALCON_SCAN_BLOCK 64
 /* The longest row of the norms. */
 #define FALCON_NORM_MAX_D 16384
 
@@ -457,7 +457,9 @@ int falcon_decode_carry_from_prefill_ex(falcon_variant variant, falcon_dtype dty
  *
  *   x, f     [N,L,D] dtype, row strides x_stride and f_stride (sequence n
  *            begins at n*L*stride): values and forget gates.  f = +inf keeps
- *            the state as it is (x finite), f = -inf replaces it.
+ *            the state as it is (x finite); from f = -80 downwards less than
+ *            2^-114 of it is left.
+ *            L is at most 2^30, N*ceil(D/32) at most 2^26.
  *   reset    [N,L] bytes, or NULL: where non-zero, token t begins a new
  *            document in a packed sequence and what came before does not
  *            reach it, whatever its value (infinities and NaN included)

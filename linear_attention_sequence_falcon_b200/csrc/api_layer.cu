@@ -42,12 +42,12 @@ int fill_f32(float *dst, const float *src, size_t n, cudaStream_t s) {
     return FALCON_ERR_LAUNCH;
 }
 
-// Grids have one axis: 256-channel-or-narrower pieces of N x blocks of tokens
-// have to stay under its limit.
+// The limit of a grid's one axis; token counts stay far enough under it that
+// a tile's tokens behind the end still have int positions.
 constexpr long long kMaxItems = 0x7fffffffll;
 
 bool scan_sizes_ok(int N, int L, int D) {
-    if (N < 0 || L < 0 || D < 0) return false;
+    if (N < 0 || L < 0 || L > (1 << 30) || D < 0) return false;
     const long long items = (long long)N * ((D + 31) / 32);
     return items <= kMaxItems / 32;
 }

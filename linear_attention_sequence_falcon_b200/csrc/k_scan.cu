@@ -1,8 +1,32 @@
 // k_scan.cu -- the gated linear recurrence (falcon_scan), its backward pass
 // and its single-token step:
-//   a_t = 1/(1+exp(-f_t)),  h_t = (reset_t ? 0 : a_t h_{t-1}) + (1-a_t) x_t.
+//   a_t = 1/(1+exp(-f_t)),  c_t = 1 - a_t,
+//   h_t = (reset_t ? 0 : a_t h_{t-1}) + c_t x_t.
 //
-// One thread per (sequence, channel) walks the tokens.
+// A run of tokens is an affine map of the state in front of it, h -> A h + B,
+// and two maps one behind the other are one: (A2 A1, A2 B1 + B2).  So the
+// tokens of one (sequence, group of channels) are cut into runs of kRun
+// tokens, one thread per run and pair of channels; a thread block takes a
+// tile of runs, and a cluster of blocks takes neighbouring tiles at once and
+// walks the sequence.  Each thread forms its run's map from registers; the
+// maps of the tile are joined through shared memory, those of the cluster's
+// tiles through distributed shared memory, one cluster barrier per step; then
+// the thread applies its map to the state that enters its run and writes.
+// Every input is read once.  The order of all joins is fixed by the token's
+// position alone, so results do not depend on the cluster's size.
+//
+// The backward pass walks the other way with the same products A:
+//   g_t = dout_t + y_t,  y_{t-1} = (reset_t ? 0 : a_t g_t),
+// whose run map is y -> A y + sum_t (a_first ... a_t) dout_t, formed in the
+// same forward loop; the states come from the marks that the forward left
+// every kScanBlock tokens.
+//
+// A map that contains a reset ignores what comes before, infinities and NaN
+// included: its A is -0.0 (no product of gates is), and it is applied by
+// selection, not by multiplication.
+#include <mutex>
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "params_layer.h"
@@ -11,94 +35,534 @@ namespace falcon {
 
 namespace {
 
-// a = sigmoid(f) and c = 1 - a, each to full relative accuracy: with e =
-// exp(-|f|) <= 1 the larger of the two is 1/(1+e), the smaller e/(1+e).
-__device__ __forceinline__ void gates(float f, float &a, float &c) {
-    const float e = expf(-fabsf(f));
-    const float big = 1.f / (1.f + e), small = e * big;
-    a = f < 0.f ? small : big;
-    c = f < 0.f ? big : small;
+constexpr int kRun = 8;        // tokens per run
+constexpr int kThreads = 256;  // 8 warps per block
+constexpr int kMaxCluster = 8;
+static_assert(kScanBlock == 8 * kRun, "a mark in front of every eighth run");
+
+// ---- pairs of fp32 in one instruction
+__device__ __forceinline__ unsigned long long bits(float2 v) { return *reinterpret_cast<unsigned long long *>(&v); }
+__device__ __forceinline__ float2 pair(unsigned long long v) { return *reinterpret_cast<float2 *>(&v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return pair(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return pair(d);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) scan_kernel(ScanParams p) {
-    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
-    if (i >= (long long)p.N * p.D) return;
-    const int n = (int)(i / p.D), ch = (int)(i % p.D);
-    const int nblk = (p.L + kScanBlock - 1) / kScanBlock;
-    float h = p.init_state ? p.init_state[i] : 0.f;
-    for (int t = 0; t < p.L; ++t) {
-        const long long row = (long long)n * p.L + t;
-        if (p.marks && t % kScanBlock == 0) p.marks[((long long)n * nblk + t / kScanBlock) * p.D + ch] = h;
-        const float x = to_f32(static_cast<const T *>(p.x)[row * p.ldx + ch]);
-        float a, c;
-        gates(to_f32(static_cast<const T *>(p.f)[row * p.ldf + ch]), a, c);
-        h = p.reset && p.reset[row] ? c * x : fmaf(a, h, c * x);
-        if (p.out) static_cast<T *>(p.out)[row * p.D + ch] = from_f32<T>(h);
+// a = sigmoid(f), c = 1 - a, each to full relative accuracy, without a branch
+// on f's sign: e = exp(-f), a = 1/(1+e), c = e a.  The exponent is held at
+// 115 (f = -79.7: a is 2e-35 from there on), so that e a stays finite.
+__device__ __forceinline__ void gates(float2 f, float2 &a, float2 &c) {
+    const float2 z = mul2(f, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    const float2 e = make_float2(ex2(min_nan(z.x, 115.f)), ex2(min_nan(z.y, 115.f)));
+    const float2 s = add2(e, make_float2(1.f, 1.f));
+    a = make_float2(rcp(s.x), rcp(s.y));
+    c = mul2(e, a);
+}
+
+// ---- loads and stores of one thread's two channels (V: next to each other
+// and aligned as a pair; otherwise `gap` apart, each by itself)
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+    float2 v;
+    __device__ __forceinline__ float2 f() const { return v; }
+    __device__ __forceinline__ void set(float x, float y) { v = make_float2(x, y); }
+};
+template <> struct Raw<__nv_bfloat16> {
+    uint32_t v;
+    __device__ __forceinline__ float2 f() const {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
     }
-    if (p.final_state) p.final_state[i] = h;
+    __device__ __forceinline__ void set(float x, float y) {  // values bf16 holds exactly
+        v = (__float_as_uint(x) >> 16) | (__float_as_uint(y) & 0xffff0000u);
+    }
+};
+
+template <typename T, bool V>
+__device__ __forceinline__ Raw<T> load_pair(const T *p, int gap, bool in0, bool in1, float fill) {
+    Raw<T> r;
+    r.set(fill, fill);
+    if constexpr (V) {
+        if (in0) r.v = *reinterpret_cast<const decltype(r.v) *>(p);
+    } else {
+        const float x = in0 ? to_f32(p[0]) : fill, y = in1 ? to_f32(p[gap]) : fill;
+        r.set(x, y);
+    }
+    return r;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) scan_bwd_kernel(ScanBwdParams p) {
-    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
-    if (i >= (long long)p.N * p.D) return;
-    const int n = (int)(i / p.D), ch = (int)(i % p.D);
+template <typename T, bool V>
+__device__ __forceinline__ void store_pair(T *p, int gap, bool in0, bool in1, float2 v) {
+    if constexpr (V) {
+        if (!in0) return;
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<__nv_bfloat162 *>(p) = __float22bfloat162_rn(v);
+        else
+            *reinterpret_cast<float2 *>(p) = v;
+    } else {
+        if (in0) p[0] = from_f32<T>(v.x);
+        if (in1) p[gap] = from_f32<T>(v.y);
+    }
+}
+
+// ---- affine maps of a pair of channels
+struct Map {
+    float2 a, b;
+};
+__device__ __forceinline__ bool cuts(float a) { return __float_as_uint(a) == 0x80000000u; }
+// m applied to h (R: m may contain a reset)
+template <bool R> __device__ __forceinline__ float2 apply(const Map &m, float2 h) {
+    float2 v = fma2(m.a, h, m.b);
+    if constexpr (R) {
+        if (cuts(m.a.x)) v.x = m.b.x;
+        if (cuts(m.a.y)) v.y = m.b.y;
+    }
+    return v;
+}
+// `after` behind `before`, as one map
+template <bool R> __device__ __forceinline__ Map join(const Map &after, const Map &before) {
+    Map m;
+    m.b = apply<R>(after, before.b);
+    m.a = mul2(after.a, before.a);
+    if constexpr (R) {
+        if (cuts(after.a.x)) m.a.x = after.a.x;
+        if (cuts(after.a.y)) m.a.y = after.a.y;
+    }
+    return m;
+}
+__device__ __forceinline__ Map unit() { return {make_float2(1.f, 1.f), make_float2(0.f, 0.f)}; }
+
+__device__ __forceinline__ Map load_map(const float4 *p) {
+    const float4 v = *p;
+    return {make_float2(v.x, v.y), make_float2(v.z, v.w)};
+}
+__device__ __forceinline__ float4 as4(const Map &m) { return make_float4(m.a.x, m.a.y, m.b.x, m.b.y); }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// writes v at `p` of this block's shared memory in the shared memory of `rank`
+__device__ __forceinline__ void store_remote(const float4 *p, uint32_t rank, float4 v) {
+    uint32_t to;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+// Which of the run's kRun tokens begin a document, as bits; the LPR lanes of
+// a run look at its bytes together.
+template <int LPR>
+__device__ __forceinline__ uint32_t reset_bits(const unsigned char *reset, long long row, int left, int lane) {
+    const int l = lane % LPR, base = lane - l;
+    uint32_t got = 0;
+#pragma unroll
+    for (int i = 0; i < kRun; i += LPR) {
+        const int t = i + l;
+        const bool set = t < kRun && t < left && reset[row + t] != 0;
+        got |= ((__ballot_sync(0xffffffffu, set) >> base) & (LPR >= 32 ? 0xffffffffu : (1u << LPR) - 1u)) << i;
+    }
+    return got & ((1u << kRun) - 1u);
+}
+
+// The place of a thread: LPR lanes, a pair of channels each, per run; 32/LPR
+// runs per warp.
+template <int LPR> struct Place {
+    static constexpr int kChannels = 2 * LPR;
+    static constexpr int kRuns = kThreads / LPR;      // per tile
+    static constexpr int kTile = kRuns * kRun;        // tokens
+};
+
+template <typename T, bool V, int LPR, bool R>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) scan_kernel(ScanParams p) {
+    using G = Place<LPR>;
+    __shared__ float4 agg[2][kThreads];
+    __shared__ float4 cl[2][kMaxCluster][LPR];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, u = threadIdx.x / LPR;
+    const int cs = (int)cluster_size(), rank = (int)cluster_rank();
+    if (cs > 1) cluster_arrive();
+    const int groups = (p.D + G::kChannels - 1) / G::kChannels;
+    const int unit_id = blockIdx.x / cs, n = unit_id / groups;
+    const int ch = (unit_id % groups) * G::kChannels + (V ? 2 * l : l);
+    constexpr int gap = LPR;
+    const bool in0 = ch < p.D, in1 = V ? in0 : ch + gap < p.D;
     const int nblk = (p.L + kScanBlock - 1) / kScanBlock;
-    float g = p.dstate ? p.dstate[i] : 0.f;
-    for (int b = nblk - 1; b >= 0; --b) {
-        const int t0 = b * kScanBlock, len = min(kScanBlock, p.L - t0);
-        float before[kScanBlock];  // the state before each of the block's tokens
-        float h = p.marks[((long long)n * nblk + b) * p.D + ch];
-        for (int t = 0; t < len; ++t) {
-            const long long row = (long long)n * p.L + t0 + t;
-            const float x = to_f32(static_cast<const T *>(p.x)[row * p.ldx + ch]);
-            float a, c;
-            gates(to_f32(static_cast<const T *>(p.f)[row * p.ldf + ch]), a, c);
-            const bool r = p.reset && p.reset[row];
-            before[t] = r ? 0.f : h;
-            h = r ? c * x : fmaf(a, h, c * x);
+    const int tiles = (p.L + G::kTile - 1) / G::kTile, steps = (tiles + cs - 1) / cs;
+    const T *x = static_cast<const T *>(p.x) + (long long)n * p.L * p.ldx + ch;
+    const T *f = static_cast<const T *>(p.f) + (long long)n * p.L * p.ldf + ch;
+    T *out = p.out ? static_cast<T *>(p.out) + (long long)n * p.L * p.D + ch : nullptr;
+    const float *init = p.init_state ? p.init_state + (long long)n * p.D + ch : nullptr;
+
+    float2 carry = make_float2(init && in0 ? init[0] : 0.f, init && in1 ? init[V ? 1 : gap] : 0.f);
+    Raw<T> rx[kRun], rf[kRun];
+    uint32_t rr = 0;
+    auto fetch = [&](int step) {
+        const int t0 = (step * cs + rank) * G::kTile + u * kRun;
+        if (step >= steps) return;
+        if constexpr (R) rr = reset_bits<LPR>(p.reset, (long long)n * p.L + t0, p.L - t0, lane);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            // tokens behind the end keep the state: f = +inf
+            const bool in = t0 + i < p.L;
+            rx[i] = load_pair<T, V>(x + (t0 + i) * p.ldx, gap, in && in0, in && in1, 0.f);
+            rf[i] = load_pair<T, V>(f + (t0 + i) * p.ldf, gap, in && in0, in && in1, __int_as_float(0x7f800000));
         }
-        for (int t = len - 1; t >= 0; --t) {
-            const long long row = (long long)n * p.L + t0 + t;
-            const float x = to_f32(static_cast<const T *>(p.x)[row * p.ldx + ch]);
-            float a, c;
-            gates(to_f32(static_cast<const T *>(p.f)[row * p.ldf + ch]), a, c);
-            g += to_f32(static_cast<const T *>(p.dout)[row * p.D + ch]);
-            static_cast<T *>(p.dx)[row * p.lddx + ch] = from_f32<T>(g * c);
-            static_cast<T *>(p.df)[row * p.lddf + ch] = from_f32<T>(g * (before[t] - x) * (a * c));
-            g = p.reset && p.reset[row] ? 0.f : a * g;
+    };
+    fetch(0);
+    for (int step = 0; step < steps; ++step) {
+        const int t0 = (step * cs + rank) * G::kTile + u * kRun, par = step & 1;
+        // the run from a zero state: pa = product of the gates up to here, hl = the state
+        float2 pa[kRun], hl[kRun];
+        const uint32_t cut = rr;
+        const int first = R && cut ? __ffs(cut) - 1 : kRun;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            float2 a, c;
+            gates(rf[i].f(), a, c);
+            const float2 b = mul2(c, rx[i].f());
+            const bool r = R && (cut >> i & 1);
+            hl[i] = i == 0 || r ? b : fma2(a, hl[i - 1], b);
+            pa[i] = i == 0 ? a : mul2(a, pa[i - 1]);
+            if (R && i >= first) pa[i] = make_float2(-0.f, -0.f);
+        }
+        agg[par][threadIdx.x] = as4({pa[kRun - 1], hl[kRun - 1]});
+        fetch(step + 1);
+        __syncthreads();
+        // the map in front of this run, and the tile's
+        Map before = unit(), all = unit();
+#pragma unroll 8
+        for (int i = 0; i < G::kRuns; ++i) {
+            if (i == u) before = all;
+            all = join<R>(load_map(&agg[par][i * LPR + l]), all);
+        }
+        float2 h = carry;
+        if (cs > 1) {
+            if (step == 0) cluster_wait();  // every block of the cluster runs before its memory is written
+            if (warp < cs && lane < LPR) store_remote(&cl[par][rank][l], warp, as4(all));
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+            float2 mine = h;
+            for (int i = 0; i < cs; ++i) {
+                if (i == rank) mine = h;
+                h = apply<R>(load_map(&cl[par][i][l]), h);
+            }
+            carry = h;
+            h = mine;
+        } else {
+            carry = apply<R>(all, h);
+        }
+        h = apply<R>(before, h);
+        if (p.marks && u % 8 == 0 && t0 < p.L)
+            store_pair<float, false>(p.marks + ((long long)n * nblk + t0 / kScanBlock) * p.D + ch, V ? 1 : gap, in0,
+                                     in1, h);
+        if (out) {
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                const float2 v = R && i >= first ? hl[i] : fma2(pa[i], h, hl[i]);
+                if (t0 + i < p.L) store_pair<T, V>(out + (long long)(t0 + i) * p.D, gap, in0, in1, v);
+            }
         }
     }
-    if (p.dinitial) p.dinitial[i] = g;
+    if (p.final_state && rank == 0 && threadIdx.x < LPR)
+        store_pair<float, false>(p.final_state + (long long)n * p.D + ch, V ? 1 : gap, in0, in1, carry);
 }
 
-template <typename T>
+template <typename T, bool V, int LPR, bool R>
+__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanBwdParams p) {
+    using G = Place<LPR>;
+    constexpr bool kAhead = sizeof(T) == 2;  // the next tile's loads before this one's barriers (fp32: no registers)
+    __shared__ float4 agg[2][kThreads];      // product of the gates, y's map
+    __shared__ float2 fwd[2][kThreads];      // the state's B
+    __shared__ float4 cl[2][kMaxCluster][LPR];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, u = threadIdx.x / LPR;
+    const int cs = (int)cluster_size(), rank = (int)cluster_rank();
+    if (cs > 1) cluster_arrive();
+    const int groups = (p.D + G::kChannels - 1) / G::kChannels;
+    const int unit_id = blockIdx.x / cs, n = unit_id / groups;
+    const int ch = (unit_id % groups) * G::kChannels + (V ? 2 * l : l);
+    constexpr int gap = LPR;
+    const bool in0 = ch < p.D, in1 = V ? in0 : ch + gap < p.D;
+    const int nblk = (p.L + kScanBlock - 1) / kScanBlock;
+    const int tiles = (p.L + G::kTile - 1) / G::kTile, steps = (tiles + cs - 1) / cs;
+    const T *x = static_cast<const T *>(p.x) + (long long)n * p.L * p.ldx + ch;
+    const T *f = static_cast<const T *>(p.f) + (long long)n * p.L * p.ldf + ch;
+    const T *dout = static_cast<const T *>(p.dout) + (long long)n * p.L * p.D + ch;
+    T *dx = static_cast<T *>(p.dx) + (long long)n * p.L * p.lddx + ch;
+    T *df = static_cast<T *>(p.df) + (long long)n * p.L * p.lddf + ch;
+    const float *ds = p.dstate ? p.dstate + (long long)n * p.D + ch : nullptr;
+
+    float2 carry = make_float2(ds && in0 ? ds[0] : 0.f, ds && in1 ? ds[V ? 1 : gap] : 0.f);
+    Raw<T> rx[kRun], rf[kRun], rd[kRun];
+    float2 rm = make_float2(0.f, 0.f);
+    uint32_t rr = 0;
+    auto fetch = [&](int step) {  // steps from the last tokens to the first
+        if (step < 0) return;
+        const int t0 = (step * cs + rank) * G::kTile + u * kRun;
+        if constexpr (R) rr = reset_bits<LPR>(p.reset, (long long)n * p.L + t0, p.L - t0, lane);
+        const Raw<float> m = load_pair<float, false>(
+            p.marks + ((long long)n * nblk + t0 / kScanBlock) * p.D + ch, V ? 1 : gap, t0 < p.L && in0,
+            t0 < p.L && in1, 0.f);
+        rm = m.v;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            // tokens behind the end hand y on: f = +inf, dout = 0
+            const bool in = t0 + i < p.L;
+            rx[i] = load_pair<T, V>(x + (t0 + i) * p.ldx, gap, in && in0, in && in1, 0.f);
+            rf[i] = load_pair<T, V>(f + (t0 + i) * p.ldf, gap, in && in0, in && in1, __int_as_float(0x7f800000));
+            rd[i] = load_pair<T, V>(dout + (long long)(t0 + i) * p.D, gap, in && in0, in && in1, 0.f);
+        }
+    };
+    if constexpr (kAhead) fetch(steps - 1);
+    for (int step = steps - 1; step >= 0; --step) {
+        const int t0 = (step * cs + rank) * G::kTile + u * kRun, par = step & 1;
+        if constexpr (!kAhead) fetch(step);
+        const uint32_t cut = rr;
+        const int first = R && cut ? __ffs(cut) - 1 : kRun;
+        const float2 mark = rm;
+        float2 a[kRun], c[kRun], q[kRun];  // q: c x, later a c (h - x)
+        Raw<T> dy[kRun];
+        float2 pa, hl, yl = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            gates(rf[i].f(), a[i], c[i]);
+            q[i] = mul2(c[i], rx[i].f());
+            dy[i] = rd[i];
+            const bool r = R && (cut >> i & 1);
+            hl = i == 0 || r ? q[i] : fma2(a[i], hl, q[i]);
+            pa = i == 0 ? a[i] : mul2(a[i], pa);
+            if (R && i >= first) pa = make_float2(-0.f, -0.f);
+            else yl = fma2(pa, dy[i].f(), yl);
+        }
+        agg[par][threadIdx.x] = as4({pa, yl});
+        fwd[par][threadIdx.x] = hl;
+        if constexpr (kAhead) fetch(step - 1);
+        __syncthreads();
+        // the state in front of this run, from the mark of its eight
+        float2 h = mark;
+        const int u0 = u & ~7;
+#pragma unroll
+        for (int i = 0; i < 7; ++i) {
+            if (u0 + i < u) {
+                const Map m = load_map(&agg[par][(u0 + i) * LPR + l]);
+                h = apply<R>({m.a, fwd[par][(u0 + i) * LPR + l]}, h);
+            }
+        }
+        // y's map behind this run, and the tile's
+        Map behind = unit(), all = unit();
+#pragma unroll 8
+        for (int i = G::kRuns - 1; i >= 0; --i) {
+            if (i == u) behind = all;
+            all = join<R>(load_map(&agg[par][i * LPR + l]), all);
+        }
+        float2 y = carry;
+        if (cs > 1) {
+            if (step == steps - 1) cluster_wait();  // every block of the cluster runs before its memory is written
+            if (warp < cs && lane < LPR) store_remote(&cl[par][rank][l], warp, as4(all));
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+            float2 mine = y;
+            for (int i = cs - 1; i >= 0; --i) {
+                if (i == rank) mine = y;
+                y = apply<R>(load_map(&cl[par][i][l]), y);
+            }
+            carry = y;
+            y = mine;
+        } else {
+            carry = apply<R>(all, y);
+        }
+        y = apply<R>(behind, y);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            const bool r = R && (cut >> i & 1);
+            const float2 hp = r ? make_float2(0.f, 0.f) : h;
+            const float2 b = q[i];
+            q[i] = mul2(a[i], fma2(c[i], hp, make_float2(-b.x, -b.y)));
+            h = r ? b : fma2(a[i], h, b);
+        }
+#pragma unroll
+        for (int i = kRun - 1; i >= 0; --i) {
+            const float2 g = add2(dy[i].f(), y);
+            if (t0 + i < p.L) {
+                store_pair<T, V>(dx + (t0 + i) * p.lddx, gap, in0, in1, mul2(g, c[i]));
+                store_pair<T, V>(df + (t0 + i) * p.lddf, gap, in0, in1, mul2(g, q[i]));
+            }
+            y = R && (cut >> i & 1) ? make_float2(0.f, 0.f) : mul2(a[i], g);
+        }
+    }
+    if (p.dinitial && rank == 0 && threadIdx.x < LPR)
+        store_pair<float, false>(p.dinitial + (long long)n * p.D + ch, V ? 1 : gap, in0, in1, carry);
+}
+
+template <typename T, bool V>
 __global__ void __launch_bounds__(128) scan_step_kernel(ScanStepParams p) {
+    const int pairs = (p.D + 1) / 2;
     const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
-    if (i >= (long long)p.N * p.D) return;
-    const int n = (int)(i / p.D), ch = (int)(i % p.D);
-    float a, c;
-    gates(to_f32(static_cast<const T *>(p.f)[n * p.ldf + ch]), a, c);
-    const float h = fmaf(a, p.state[i], c * to_f32(static_cast<const T *>(p.x)[n * p.ldx + ch]));
-    p.state_out[i] = h;
-    static_cast<T *>(p.out)[i] = from_f32<T>(h);
+    if (i >= (long long)p.N * pairs) return;
+    const int n = (int)(i / pairs), ch = 2 * (int)(i % pairs);
+    const bool in1 = ch + 1 < p.D;
+    const long long at = (long long)n * p.D + ch;
+    const float2 x = load_pair<T, V>(static_cast<const T *>(p.x) + n * p.ldx + ch, 1, true, in1, 0.f).f();
+    const float2 f = load_pair<T, V>(static_cast<const T *>(p.f) + n * p.ldf + ch, 1, true, in1, 0.f).f();
+    const float2 s = load_pair<float, V>(p.state + at, 1, true, in1, 0.f).f();
+    float2 a, c;
+    gates(f, a, c);
+    const float2 h = fma2(a, s, mul2(c, x));
+    store_pair<float, V>(p.state_out + at, 1, true, in1, h);
+    store_pair<T, V>(static_cast<T *>(p.out) + at, 1, true, in1, h);
 }
 
-unsigned blocks(long long items) { return (unsigned)((items + 127) / 128); }
+// ---- launches
+
+bool pair_aligned(const void *p, size_t elt, long long ld) {
+    return (reinterpret_cast<uintptr_t>(p) & (2 * elt - 1)) == 0 && ld % 2 == 0;
+}
+
+// How many clusters of `cs` blocks of a kernel the device holds at once, from
+// the occupancy calculator, kept per (kernel, device, cs).
+template <typename K> int clusters_held(K kernel, int cs) {
+    constexpr int kDevices = 16;
+    static std::mutex guard;
+    static struct { const void *k; int held[kDevices][kMaxCluster + 1]; } kept[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 148 * 2 / cs;
+    std::lock_guard<std::mutex> lock(guard);
+    int *slot = nullptr;
+    for (auto &e : kept) {
+        if (e.k == nullptr) e.k = reinterpret_cast<const void *>(kernel);
+        if (e.k == reinterpret_cast<const void *>(kernel)) { slot = &e.held[dev][cs]; break; }
+    }
+    if (slot && *slot) return *slot;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(cs * 148);
+    c.blockDim = dim3(kThreads);
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cs; at.val.clusterDim.y = 1; at.val.clusterDim.z = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    int held = 0;
+    if (cudaOccupancyMaxActiveClusters(&held, kernel, &c) != cudaSuccess || held < 1) {
+        cudaGetLastError();
+        held = 1;
+    }
+    if (slot) *slot = held;
+    return held;
+}
+
+// The cluster's size: blocks walk steps = tiles/cs tiles each, in as many
+// waves as the device needs for all units' clusters; the size with the least
+// waves x steps, the smallest of equals (a smaller cluster joins fewer maps).
+template <typename K> int pick_cluster(K kernel, long long units, int tiles) {
+    int best = 1;
+    long long cost = 0;
+    for (int cs = 1; cs <= kMaxCluster && cs <= tiles; ++cs) {
+        const long long waves = (units + clusters_held(kernel, cs) - 1) / clusters_held(kernel, cs);
+        const long long here = waves * ((tiles + cs - 1) / cs);
+        if (cs == 1 || here < cost) { best = cs; cost = here; }
+    }
+    return best;
+}
+
+template <typename K, typename P> int launch_units(K kernel, const P &p, long long units, int tiles, cudaStream_t s) {
+    const int cs = pick_cluster(kernel, units, tiles);
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(units * cs));
+    c.blockDim = dim3(kThreads);
+    c.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cs; at.val.clusterDim.y = 1; at.val.clusterDim.z = 1;
+    c.attrs = &at;
+    c.numAttrs = cs > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&c, kernel, p) == cudaSuccess) return 0;
+    cudaGetLastError();
+    return -7;
+}
+
+// Lanes per run: the fewest that hold the row's pairs, 32 at most.
+template <typename F> int with_lanes(int D, F go) {
+    if (D <= 8) return go(std::integral_constant<int, 4>());
+    if (D <= 16) return go(std::integral_constant<int, 8>());
+    if (D <= 32) return go(std::integral_constant<int, 16>());
+    return go(std::integral_constant<int, 32>());
+}
+
+template <typename F> int with_bools(bool v, bool r, F go) {
+    if (v) return r ? go(std::true_type(), std::true_type()) : go(std::true_type(), std::false_type());
+    return r ? go(std::false_type(), std::true_type()) : go(std::false_type(), std::false_type());
+}
 
 }  // namespace
 
 template <typename T> int launch_scan(const ScanParams &p, cudaStream_t s) {
-    scan_kernel<T><<<blocks((long long)p.N * p.D), 128, 0, s>>>(p);
-    return 0;
+    const bool v = p.D % 2 == 0 && pair_aligned(p.x, sizeof(T), p.ldx) && pair_aligned(p.f, sizeof(T), p.ldf) &&
+                   (!p.out || pair_aligned(p.out, sizeof(T), p.D));
+    return with_lanes(p.D, [&](auto lpr) {
+        using G = Place<decltype(lpr)::value>;
+        const long long units = (long long)p.N * ((p.D + G::kChannels - 1) / G::kChannels);
+        return with_bools(v, p.reset != nullptr, [&](auto vv, auto rr) {
+            return launch_units(scan_kernel<T, decltype(vv)::value, decltype(lpr)::value, decltype(rr)::value>, p,
+                                units, (p.L + G::kTile - 1) / G::kTile, s);
+        });
+    });
 }
+
 template <typename T> int launch_scan_bwd(const ScanBwdParams &p, cudaStream_t s) {
-    scan_bwd_kernel<T><<<blocks((long long)p.N * p.D), 128, 0, s>>>(p);
-    return 0;
+    const bool v = p.D % 2 == 0 && pair_aligned(p.x, sizeof(T), p.ldx) && pair_aligned(p.f, sizeof(T), p.ldf) &&
+                   pair_aligned(p.dout, sizeof(T), p.D) && pair_aligned(p.dx, sizeof(T), p.lddx) &&
+                   pair_aligned(p.df, sizeof(T), p.lddf);
+    return with_lanes(p.D, [&](auto lpr) {
+        using G = Place<decltype(lpr)::value>;
+        const long long units = (long long)p.N * ((p.D + G::kChannels - 1) / G::kChannels);
+        return with_bools(v, p.reset != nullptr, [&](auto vv, auto rr) {
+            return launch_units(scan_bwd_kernel<T, decltype(vv)::value, decltype(lpr)::value, decltype(rr)::value>, p,
+                                units, (p.L + G::kTile - 1) / G::kTile, s);
+        });
+    });
 }
+
 template <typename T> int launch_scan_step(const ScanStepParams &p, cudaStream_t s) {
-    scan_step_kernel<T><<<blocks((long long)p.N * p.D), 128, 0, s>>>(p);
+    const long long pairs = (long long)p.N * ((p.D + 1) / 2);
+    const bool v = p.D % 2 == 0 && pair_aligned(p.x, sizeof(T), p.ldx) && pair_aligned(p.f, sizeof(T), p.ldf) &&
+                   pair_aligned(p.out, sizeof(T), p.D) && pair_aligned(p.state, 4, 0) && pair_aligned(p.state_out, 4, 0);
+    const unsigned blocks = (unsigned)((pairs + 127) / 128);
+    if (v) scan_step_kernel<T, true><<<blocks, 128, 0, s>>>(p);
+    else scan_step_kernel<T, false><<<blocks, 128, 0, s>>>(p);
     return 0;
 }
 

@@ -8,7 +8,7 @@
 
 namespace falcon {
 
-constexpr int kScanBlock = 128;    // tokens between two marks (FALCON_SCAN_BLOCK)
+constexpr int kScanBlock = 64;     // tokens between two marks (FALCON_SCAN_BLOCK)
 constexpr int kNormMaxD = 16384;   // the longest row of the norms (FALCON_NORM_MAX_D)
 
 struct ScanParams {

@@ -21,7 +21,7 @@ import torch
 
 from ._lib import DTYPES, FalconError, _check, _shape_error, load
 
-SCAN_BLOCK = 128     # tokens between two marks of scan
+SCAN_BLOCK = 64      # tokens between two marks of scan
 NORM_MAX_D = 16384   # the longest row of the norms
 
 
