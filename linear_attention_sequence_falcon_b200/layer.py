@@ -25,6 +25,11 @@ SCAN_BLOCK = 64      # tokens between two marks of scan
 NORM_MAX_D = 16384   # the longest row of the norms
 
 
+_NOTHING = contextlib.nullcontext()
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream builds an object: 3 us a call
+
+
 def _on(device, stream):
     """Makes `device` current, and `stream` with it, for one call."""
     if device.type != "cuda":
@@ -33,29 +38,27 @@ def _on(device, stream):
         if stream.device != device:
             raise FalconError("the stream is on %s, the tensors on %s" % (stream.device, device))
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    return _NOTHING if device.index == _current_device() else torch.cuda.device(device)
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream():
-    return torch.cuda.current_stream().cuda_stream
+def _like(t, name, shape, dtype, device):
+    if t.shape != shape:
+        _shape_error("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype != dtype:
+        raise FalconError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise FalconError("%s is on %s, not on %s" % (name, t.device, device))
 
 
 def _need(t, name, shape, dtype, device):
     """A contiguous array of this shape, dtype and device (or None)."""
     if t is None:
         return
-    if tuple(t.shape) != shape:
-        _shape_error("%s must be %s, got %s" % (name, shape, tuple(t.shape)))
-    if t.dtype != dtype:
-        raise FalconError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device:
-        raise FalconError("%s is on %s, not on %s" % (name, t.device, device))
+    _like(t, name, shape, dtype, device)
     if not t.is_contiguous():
         raise FalconError("%s must be contiguous" % name)
 
@@ -63,12 +66,7 @@ def _need(t, name, shape, dtype, device):
 def _rows(t, name, shape, dtype, device):
     """The row stride of an array of rows: contiguous last axis, the tokens of
     all its sequences evenly spaced."""
-    if tuple(t.shape) != shape:
-        _shape_error("%s must be %s, got %s" % (name, shape, tuple(t.shape)))
-    if t.dtype != dtype:
-        raise FalconError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device:
-        raise FalconError("%s is on %s, not on %s" % (name, t.device, device))
+    _like(t, name, shape, dtype, device)
     D = shape[-1]
     if t.is_contiguous():
         return D
@@ -76,12 +74,13 @@ def _rows(t, name, shape, dtype, device):
     if D > 1 and st[-1] != 1:
         raise FalconError("the last axis of %s must be contiguous" % name)
     step, span = None, 1  # tokens covered by the axes seen so far, from the last one outwards
-    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
+    for i in range(len(shape) - 2, -1, -1):
+        n = shape[i]
         if n == 1:
             continue
         if step is None:
-            step = s
-        elif s != step * span:
+            step = st[i]
+        elif st[i] != step * span:
             raise FalconError("the rows of %s must be evenly spaced (strides %s)" % (name, st))
         span *= n
     if step is not None and step < D:
@@ -135,7 +134,7 @@ def check_scan_shapes(x, f, reset=None, initial_state=None, out=None, final_stat
     if x.dim() != 3:
         _shape_error("x must be [N,L,D], got %s" % (tuple(x.shape),))
     _dtype(x, "x")
-    shape = N, L, D = tuple(x.shape)
+    shape = N, L, D = x.shape
     dev = x.device
     ldx = _rows(x, "x", shape, x.dtype, dev)
     ldf = _rows(f, "f", shape, x.dtype, dev)
@@ -145,7 +144,8 @@ def check_scan_shapes(x, f, reset=None, initial_state=None, out=None, final_stat
         _need(reset, "reset", (N, L), reset.dtype, dev)
     for t, name in ((initial_state, "initial_state"), (final_state, "final_state"), (dstate, "dstate")):
         _need(t, name, (N, D), torch.float32, dev)
-    _need(marks, "marks", (N, -(-L // SCAN_BLOCK), D), torch.float32, dev)
+    if marks is not None:
+        _need(marks, "marks", (N, -(-L // SCAN_BLOCK), D), torch.float32, dev)
     _need(out, "out", shape, x.dtype, dev)
     _need(dout, "dout", shape, x.dtype, dev)
     for t, name in ((dx, "dx"), (df, "df")):
@@ -164,15 +164,16 @@ def scan(x, f, reset=None, initial_state=None, out=None, final_state=None, marks
     marks)."""
     lib = load()
     N, L, D, ldx, ldf = check_scan_shapes(x, f, reset, initial_state, out, final_state, marks)
-    with _on(x.device, stream):
+    dev = x.device
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((N, L, D), dtype=x.dtype, device=x.device)
+            out = x.new_empty(x.shape)
         if final_state is None and want_state:
-            final_state = torch.empty((N, D), dtype=torch.float32, device=x.device)
+            final_state = x.new_empty((N, D), dtype=torch.float32)
         if marks is None and want_marks:
-            marks = torch.empty((N, -(-L // SCAN_BLOCK), D), dtype=torch.float32, device=x.device)
+            marks = x.new_empty((N, -(-L // SCAN_BLOCK), D), dtype=torch.float32)
         _check(lib.falcon_scan(DTYPES[x.dtype], _p(x), _p(f), _p(reset), _p(initial_state), N, L, D, ldx, ldf,
-                               _p(out), _p(final_state), _p(marks), _raw_stream()))
+                               _p(out), _p(final_state), _p(marks), _raw_stream(dev.index)))
     return (out, final_state, marks) if want_marks else (out, final_state)
 
 
@@ -192,19 +193,23 @@ def scan_bwd(x, f, dout, dstate=None, reset=None, initial_state=None, marks=None
     and dinitial [N,D] fp32."""
     lib = load()
     N, L, D, ldx, ldf = check_scan_shapes(x, f, reset, initial_state, None, None, marks, dout, dstate, dx, df)
-    with _on(x.device, stream):
+    dev = x.device
+    with _on(dev, stream):
+        lddx = lddf = D
         if dx is None:
-            dx = torch.empty((N, L, D), dtype=x.dtype, device=x.device)
+            dx = x.new_empty(x.shape)
+        else:
+            lddx = _rows(dx, "dx", x.shape, x.dtype, dev)
         if df is None:
-            df = torch.empty((N, L, D), dtype=x.dtype, device=x.device)
-        dinitial = torch.empty((N, D), dtype=torch.float32, device=x.device)
+            df = x.new_empty(x.shape)
+        else:
+            lddf = _rows(df, "df", x.shape, x.dtype, dev)
+        dinitial = x.new_empty((N, D), dtype=torch.float32)
         need = 0 if marks is not None else scan_bwd_workspace_size(x.dtype, N, L, D, False)
-        ws, have = _workspace(need, workspace, x.device)
+        ws, have = _workspace(need, workspace, dev)
         _check(lib.falcon_scan_bwd_ws(DTYPES[x.dtype], _p(x), _p(f), _p(reset), _p(initial_state), _p(marks), N, L,
-                                      D, ldx, ldf, _p(dout), _p(dstate), _p(dx),
-                                      _rows(dx, "dx", (N, L, D), x.dtype, x.device), _p(df),
-                                      _rows(df, "df", (N, L, D), x.dtype, x.device), _p(dinitial), _p(ws), have,
-                                      _raw_stream()))
+                                      D, ldx, ldf, _p(dout), _p(dstate), _p(dx), lddx, _p(df), lddf, _p(dinitial),
+                                      _p(ws), have, _raw_stream(dev.index)))
     return {"dx": dx, "df": df, "dinitial": dinitial}
 
 
@@ -216,7 +221,7 @@ def scan_step(x, f, state, state_out=None, out=None, stream=None):
     if x.dim() != 2:
         _shape_error("x must be [N,D], got %s" % (tuple(x.shape),))
     dt = _dtype(x, "x")
-    shape = N, D = tuple(x.shape)
+    shape = N, D = x.shape
     dev = x.device
     ldx = _rows(x, "x", shape, x.dtype, dev)
     ldf = _rows(f, "f", shape, x.dtype, dev)
@@ -227,9 +232,9 @@ def scan_step(x, f, state, state_out=None, out=None, stream=None):
     _need(out, "out", shape, x.dtype, dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(shape, dtype=x.dtype, device=dev)
+            out = x.new_empty(shape)
         _check(lib.falcon_scan_step(dt, _p(x), _p(f), _p(state), N, D, ldx, ldf, _p(state_out), _p(out),
-                                    _raw_stream()))
+                                    _raw_stream(dev.index)))
     return out, state_out
 
 
@@ -276,13 +281,14 @@ def norm_gate(o, gate, weight, eps: float, out=None, stream=None):
     lib = load()
     B, H, L, d, ldg = check_norm_gate_shapes(o, gate, weight, out)
     eps = _eps(eps)
-    with _on(o.device, stream):
+    dev = o.device
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((B, L, H * d), dtype=o.dtype, device=o.device)
+            out = o.new_empty((B, L, H * d))
         sb, sh, sl, _ = o.stride()
         _check(lib.falcon_norm_gate(DTYPES[o.dtype], _p(o), sb, sh, sl, _p(gate), ldg, _p(weight),
                                     int(weight is not None and weight.dim() == 2), eps, B, H, L, d, _p(out),
-                                    _raw_stream()))
+                                    _raw_stream(dev.index)))
     return out
 
 
@@ -305,20 +311,23 @@ def norm_gate_bwd(o, gate, weight, eps: float, dout, do=None, dgate=None, want_d
     if gate is None and dgate is not None:
         raise FalconError("dgate without a gate")
     eps = _eps(eps)
-    with _on(o.device, stream):
+    dev = o.device
+    with _on(dev, stream):
+        lddg = H * d
         if do is None:
-            do = torch.empty((B, H, L, d), dtype=o.dtype, device=o.device)
-        if dgate is None and gate is not None:
-            dgate = torch.empty((B, L, H * d), dtype=o.dtype, device=o.device)
-        lddg = H * d if dgate is None else _rows(dgate, "dgate", (B, L, H * d), o.dtype, o.device)
+            do = o.new_empty((B, H, L, d))
+        if dgate is not None:
+            lddg = _rows(dgate, "dgate", (B, L, H * d), o.dtype, dev)
+        elif gate is not None:
+            dgate = o.new_empty((B, L, H * d))
         dweight = torch.empty_like(weight) if weight is not None and want_dweight else None
-        ws, have = _workspace(norm_gate_bwd_workspace_size(o.dtype, B, H, L, d), workspace, o.device)
+        ws, have = _workspace(norm_gate_bwd_workspace_size(o.dtype, B, H, L, d), workspace, dev)
         sb, sh, sl, _ = o.stride()
         tb, th, tl, _ = do.stride()
         _check(lib.falcon_norm_gate_bwd_ws(DTYPES[o.dtype], _p(o), sb, sh, sl, _p(gate), ldg, _p(weight),
                                            int(weight is not None and weight.dim() == 2), eps, B, H, L, d, _p(dout),
                                            _p(do), tb, th, tl, _p(dgate), lddg, _p(dweight), _p(ws), have,
-                                           _raw_stream()))
+                                           _raw_stream(dev.index)))
     return {"do": do, "dgate": dgate, "dweight": dweight}
 
 
@@ -331,7 +340,7 @@ def check_residual_norm_shapes(r, weight, y=None, scale=None, **like_r):
     if r.dim() < 1:
         _shape_error("r must be [..., D]")
     _dtype(r, "r")
-    shape, dev = tuple(r.shape), r.device
+    shape, dev = r.shape, r.device
     D = shape[-1]
     if not 1 <= D <= NORM_MAX_D:
         _shape_error("the rows must have 1 to %d channels, got %d" % (NORM_MAX_D, D))
@@ -356,14 +365,15 @@ def residual_norm(r, weight, eps: float, y=None, scale=None, r_out=None, h=None,
     eps = _eps(eps)
     if h is not None and r_out is not None and h.data_ptr() == r_out.data_ptr() and R:
         raise FalconError("h and r_out are the same array")
-    with _on(r.device, stream):
+    dev = r.device
+    with _on(dev, stream):
         if h is None:
-            h = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+            h = torch.empty_like(r)
         write = r_out
         if y is not None and r_out is None:
-            write = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+            write = torch.empty_like(r)
         _check(lib.falcon_residual_norm(DTYPES[r.dtype], _p(r), _p(y), _p(scale), _p(weight), eps, R, D, _p(write),
-                                        _p(h), _raw_stream()))
+                                        _p(h), _raw_stream(dev.index)))
     return (r if write is None else write), h
 
 
@@ -388,16 +398,17 @@ def residual_norm_bwd(r_out, weight, eps: float, dh, dr_out=None, y=None, scale=
         raise FalconError("without a scale dy is dr: it is not written apart")
     if dr is not None and dy is not None and dr.data_ptr() == dy.data_ptr() and R:
         raise FalconError("dr and dy are the same array")
-    with _on(r_out.device, stream):
+    dev = r_out.device
+    with _on(dev, stream):
         if dr is None:
-            dr = torch.empty(r_out.shape, dtype=r_out.dtype, device=r_out.device)
+            dr = torch.empty_like(r_out)
         if dy is None and scale is not None:
-            dy = torch.empty(r_out.shape, dtype=r_out.dtype, device=r_out.device)
+            dy = torch.empty_like(r_out)
         dscale = None if scale is None else torch.empty_like(scale)
         dweight = None if weight is None else torch.empty_like(weight)
-        ws, have = _workspace(residual_norm_bwd_workspace_size(r_out.dtype, R, D), workspace, r_out.device)
+        ws, have = _workspace(residual_norm_bwd_workspace_size(r_out.dtype, R, D), workspace, dev)
         _check(lib.falcon_residual_norm_bwd_ws(DTYPES[r_out.dtype], _p(r_out), _p(y), _p(scale), _p(weight), _p(dh),
                                                _p(dr_out), eps, R, D, _p(dr), _p(dy), _p(dscale), _p(dweight),
-                                               _p(ws), have, _raw_stream()))
+                                               _p(ws), have, _raw_stream(dev.index)))
     return {"dr": dr, "dy": dy if scale is not None else (dr if y is not None else None), "dscale": dscale,
             "dweight": dweight}
