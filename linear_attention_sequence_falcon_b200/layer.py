@@ -11,11 +11,15 @@ made here then belong to that stream), and return without synchronising; work
 that made the inputs on another stream is the caller's to wait for.  Rows are
 read through a row stride where the arguments say "rows": [.., L, D] with a
 contiguous last axis whose tokens lie evenly, such as half of a projection.
+
+The small calls are bound by the host (one kernel of 2-3 us behind each), so
+the checks take the short way: sizes, dtype, device index and contiguity in
+one expression, and the words for a refusal only when there is one.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -24,49 +28,48 @@ from ._lib import DTYPES, FalconError, _check, _shape_error, load
 SCAN_BLOCK = 64      # tokens between two marks of scan
 NORM_MAX_D = 16384   # the longest row of the norms
 
-
-_NOTHING = contextlib.nullcontext()
+_F32 = torch.float32
 _current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream builds an object: 3 us a call
 
 
-def _on(device, stream):
-    """Makes `device` current, and `stream` with it, for one call."""
-    if device.type != "cuda":
+def _elsewhere(index, stream):
+    """Whether the call has to change the current device or stream first."""
+    if index < 0:
         raise FalconError("tensor is not on a CUDA device (no CPU path exists)")
-    if stream is not None:
-        if stream.device != device:
-            raise FalconError("the stream is on %s, the tensors on %s" % (stream.device, device))
-        return torch.cuda.stream(stream)
-    return _NOTHING if device.index == _current_device() else torch.cuda.device(device)
+    return stream is not None or index != _current_device()
 
 
-def _p(t):
-    return None if t is None else t.data_ptr()
+def _on(t, stream):
+    """Makes the tensor's device current, and the stream with it."""
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise FalconError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
+    return torch.cuda.stream(stream)
 
 
-def _like(t, name, shape, dtype, device):
+def _refuse(t, name, shape, dtype, index):
     if t.shape != shape:
         _shape_error("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise FalconError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device:
-        raise FalconError("%s is on %s, not on %s" % (name, t.device, device))
+    if t.get_device() != index:
+        raise FalconError("every tensor must be on one device (%s is on %s)" % (name, t.device))
+    raise FalconError("%s must be contiguous" % name)
 
 
-def _need(t, name, shape, dtype, device):
-    """A contiguous array of this shape, dtype and device (or None)."""
-    if t is None:
-        return
-    _like(t, name, shape, dtype, device)
-    if not t.is_contiguous():
-        raise FalconError("%s must be contiguous" % name)
+def _need(t, name, shape, dtype, index):
+    """A contiguous array of this shape, dtype and device."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, index)
 
 
-def _rows(t, name, shape, dtype, device):
+def _rows(t, name, shape, dtype, index):
     """The row stride of an array of rows: contiguous last axis, the tokens of
     all its sequences evenly spaced."""
-    _like(t, name, shape, dtype, device)
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        _refuse(t, name, shape, dtype, index)
     D = shape[-1]
     if t.is_contiguous():
         return D
@@ -83,9 +86,11 @@ def _rows(t, name, shape, dtype, device):
         elif st[i] != step * span:
             raise FalconError("the rows of %s must be evenly spaced (strides %s)" % (name, st))
         span *= n
-    if step is not None and step < D:
+    if step is None:
+        return D
+    if step < D:
         raise FalconError("the rows of %s overlap (strides %s)" % (name, st))
-    return D if step is None else step
+    return step
 
 
 def _apart(t, name):
@@ -103,13 +108,17 @@ def _dtype(t, name):
     return DTYPES[t.dtype]
 
 
-def _workspace(need, workspace, device):
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(need, workspace, like):
     if need == 0:
         return None, 0
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device), need
-    if workspace.device != device or not workspace.is_contiguous():
-        raise FalconError("workspace must be a contiguous array on %s" % (device,))
+        return like.new_empty(need, dtype=torch.uint8), need
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise FalconError("workspace must be a contiguous array on %s" % (like.device,))
     have = workspace.numel() * workspace.element_size()
     if have < need:
         raise FalconError("workspace of %d bytes is smaller than the %d the call needs" % (have, need))
@@ -133,24 +142,32 @@ def check_scan_shapes(x, f, reset=None, initial_state=None, out=None, final_stat
     contiguous.  Returns (N, L, D, row stride of x, row stride of f)."""
     if x.dim() != 3:
         _shape_error("x must be [N,L,D], got %s" % (tuple(x.shape),))
+    dt = x.dtype
     _dtype(x, "x")
     shape = N, L, D = x.shape
-    dev = x.device
-    ldx = _rows(x, "x", shape, x.dtype, dev)
-    ldf = _rows(f, "f", shape, x.dtype, dev)
+    at = x.get_device()
+    ldx = _rows(x, "x", shape, dt, at)
+    ldf = _rows(f, "f", shape, dt, at)
     if reset is not None:
         if reset.dtype not in (torch.bool, torch.uint8):
             raise FalconError("reset must be bool or uint8, got %s" % reset.dtype)
-        _need(reset, "reset", (N, L), reset.dtype, dev)
-    for t, name in ((initial_state, "initial_state"), (final_state, "final_state"), (dstate, "dstate")):
-        _need(t, name, (N, D), torch.float32, dev)
+        _need(reset, "reset", (N, L), reset.dtype, at)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", (N, D), _F32, at)
+    if final_state is not None:
+        _need(final_state, "final_state", (N, D), _F32, at)
+    if dstate is not None:
+        _need(dstate, "dstate", (N, D), _F32, at)
     if marks is not None:
-        _need(marks, "marks", (N, -(-L // SCAN_BLOCK), D), torch.float32, dev)
-    _need(out, "out", shape, x.dtype, dev)
-    _need(dout, "dout", shape, x.dtype, dev)
-    for t, name in ((dx, "dx"), (df, "df")):
-        if t is not None:
-            _rows(t, name, shape, x.dtype, dev)
+        _need(marks, "marks", (N, -(-L // SCAN_BLOCK), D), _F32, at)
+    if out is not None:
+        _need(out, "out", shape, dt, at)
+    if dout is not None:
+        _need(dout, "dout", shape, dt, at)
+    if dx is not None:
+        _rows(dx, "dx", shape, dt, at)
+    if df is not None:
+        _rows(df, "df", shape, dt, at)
     return N, L, D, ldx, ldf
 
 
@@ -162,18 +179,19 @@ def scan(x, f, reset=None, initial_state=None, out=None, final_state=None, marks
     packed into one sequence).  Returns (out, final_state), and with
     want_marks the marks that scan_bwd continues from: (out, final_state,
     marks)."""
-    lib = load()
     N, L, D, ldx, ldf = check_scan_shapes(x, f, reset, initial_state, out, final_state, marks)
-    dev = x.device
-    with _on(dev, stream):
-        if out is None:
-            out = x.new_empty(x.shape)
-        if final_state is None and want_state:
-            final_state = x.new_empty((N, D), dtype=torch.float32)
-        if marks is None and want_marks:
-            marks = x.new_empty((N, -(-L // SCAN_BLOCK), D), dtype=torch.float32)
-        _check(lib.falcon_scan(DTYPES[x.dtype], _p(x), _p(f), _p(reset), _p(initial_state), N, L, D, ldx, ldf,
-                               _p(out), _p(final_state), _p(marks), _raw_stream(dev.index)))
+    at = x.get_device()
+    if _elsewhere(at, stream):
+        with _on(x, stream):
+            return scan(x, f, reset, initial_state, out, final_state, marks, want_state, want_marks)
+    if out is None:
+        out = x.new_empty((N, L, D))
+    if final_state is None and want_state:
+        final_state = x.new_empty((N, D), dtype=_F32)
+    if marks is None and want_marks:
+        marks = x.new_empty((N, -(-L // SCAN_BLOCK), D), dtype=_F32)
+    _check(load().falcon_scan(DTYPES[x.dtype], x.data_ptr(), f.data_ptr(), _p(reset), _p(initial_state), N, L, D, ldx,
+                              ldf, out.data_ptr(), _p(final_state), _p(marks), _raw_stream(at)))
     return (out, final_state, marks) if want_marks else (out, final_state)
 
 
@@ -191,25 +209,24 @@ def scan_bwd(x, f, dout, dstate=None, reset=None, initial_state=None, marks=None
     reset and initial_state; without them they are formed again first.
     Returns a dict: dx, df [N,L,D] (written into `dx`, `df` where given: rows)
     and dinitial [N,D] fp32."""
-    lib = load()
-    N, L, D, ldx, ldf = check_scan_shapes(x, f, reset, initial_state, None, None, marks, dout, dstate, dx, df)
-    dev = x.device
-    with _on(dev, stream):
-        lddx = lddf = D
-        if dx is None:
-            dx = x.new_empty(x.shape)
-        else:
-            lddx = _rows(dx, "dx", x.shape, x.dtype, dev)
-        if df is None:
-            df = x.new_empty(x.shape)
-        else:
-            lddf = _rows(df, "df", x.shape, x.dtype, dev)
-        dinitial = x.new_empty((N, D), dtype=torch.float32)
-        need = 0 if marks is not None else scan_bwd_workspace_size(x.dtype, N, L, D, False)
-        ws, have = _workspace(need, workspace, dev)
-        _check(lib.falcon_scan_bwd_ws(DTYPES[x.dtype], _p(x), _p(f), _p(reset), _p(initial_state), _p(marks), N, L,
-                                      D, ldx, ldf, _p(dout), _p(dstate), _p(dx), lddx, _p(df), lddf, _p(dinitial),
-                                      _p(ws), have, _raw_stream(dev.index)))
+    N, L, D, ldx, ldf = check_scan_shapes(x, f, reset, initial_state, None, None, marks, dout, dstate)
+    at = x.get_device()
+    lddx = D if dx is None else _rows(dx, "dx", x.shape, x.dtype, at)
+    lddf = D if df is None else _rows(df, "df", x.shape, x.dtype, at)
+    if _elsewhere(at, stream):
+        with _on(x, stream):
+            return scan_bwd(x, f, dout, dstate, reset, initial_state, marks, dx, df, None, workspace)
+    if dx is None:
+        dx = x.new_empty((N, L, D))
+    if df is None:
+        df = x.new_empty((N, L, D))
+    dinitial = x.new_empty((N, D), dtype=_F32)
+    ws, have = None, 0
+    if marks is None:
+        ws, have = _workspace(scan_bwd_workspace_size(x.dtype, N, L, D, False), workspace, x)
+    _check(load().falcon_scan_bwd_ws(DTYPES[x.dtype], x.data_ptr(), f.data_ptr(), _p(reset), _p(initial_state),
+                                     _p(marks), N, L, D, ldx, ldf, dout.data_ptr(), _p(dstate), dx.data_ptr(), lddx,
+                                     df.data_ptr(), lddf, dinitial.data_ptr(), _p(ws), have, _raw_stream(at)))
     return {"dx": dx, "df": df, "dinitial": dinitial}
 
 
@@ -217,24 +234,27 @@ def scan_step(x, f, state, state_out=None, out=None, stream=None):
     """falcon_scan_step: one token of N sequences, x and f [N,D] (rows), state
     [N,D] fp32.  The new state is written to state_out, or over `state`
     without one.  Returns (out [N,D], the new state)."""
-    lib = load()
     if x.dim() != 2:
         _shape_error("x must be [N,D], got %s" % (tuple(x.shape),))
     dt = _dtype(x, "x")
     shape = N, D = x.shape
-    dev = x.device
-    ldx = _rows(x, "x", shape, x.dtype, dev)
-    ldf = _rows(f, "f", shape, x.dtype, dev)
+    at = x.get_device()
+    ldx = _rows(x, "x", shape, x.dtype, at)
+    ldf = _rows(f, "f", shape, x.dtype, at)
+    _need(state, "state", shape, _F32, at)
     if state_out is None:
         state_out = state
-    _need(state, "state", shape, torch.float32, dev)
-    _need(state_out, "state_out", shape, torch.float32, dev)
-    _need(out, "out", shape, x.dtype, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = x.new_empty(shape)
-        _check(lib.falcon_scan_step(dt, _p(x), _p(f), _p(state), N, D, ldx, ldf, _p(state_out), _p(out),
-                                    _raw_stream(dev.index)))
+    else:
+        _need(state_out, "state_out", shape, _F32, at)
+    if out is not None:
+        _need(out, "out", shape, x.dtype, at)
+    if _elsewhere(at, stream):
+        with _on(x, stream):
+            return scan_step(x, f, state, state_out, out)
+    if out is None:
+        out = x.new_empty(shape)
+    _check(load().falcon_scan_step(dt, x.data_ptr(), f.data_ptr(), state.data_ptr(), N, D, ldx, ldf,
+                                   state_out.data_ptr(), out.data_ptr(), _raw_stream(at)))
     return out, state_out
 
 
@@ -251,25 +271,26 @@ def check_norm_gate_shapes(o, gate, weight, out=None, dout=None, do=None, dgate=
     B, H, L, d = o.shape
     if not 1 <= d <= NORM_MAX_D:
         _shape_error("the rows must have 1 to %d channels, got %d" % (NORM_MAX_D, d))
-    dev = o.device
-    for t, name in ((o, "o"), (do, "do")):
-        if t is not None and d > 1 and t.stride(-1) != 1:
-            raise FalconError("the last axis of %s must be contiguous" % name)
-    if do is not None and (tuple(do.shape) != (B, H, L, d) or do.dtype != o.dtype or do.device != dev):
-        _shape_error("do must be like o")
+    dt, at, shape = o.dtype, o.get_device(), (B, L, H * d)
+    if d > 1 and o.stride(3) != 1:
+        raise FalconError("the last axis of o must be contiguous")
     if do is not None:
+        if do.shape != o.shape or do.dtype is not dt or do.get_device() != at:
+            _shape_error("do must be like o")
+        if d > 1 and do.stride(3) != 1:
+            raise FalconError("the last axis of do must be contiguous")
         _apart(do, "do")
     ldg = H * d
     if gate is not None:
-        ldg = _rows(gate, "gate", (B, L, H * d), o.dtype, dev)
+        ldg = _rows(gate, "gate", shape, dt, at)
     if dgate is not None:
-        _rows(dgate, "dgate", (B, L, H * d), o.dtype, dev)
-    if weight is not None and weight.dim() == 1:
-        _need(weight, "weight", (d,), torch.float32, dev)
-    else:
-        _need(weight, "weight", (H, d), torch.float32, dev)
-    _need(out, "out", (B, L, H * d), o.dtype, dev)
-    _need(dout, "dout", (B, L, H * d), o.dtype, dev)
+        _rows(dgate, "dgate", shape, dt, at)
+    if weight is not None:
+        _need(weight, "weight", (d,) if weight.dim() == 1 else (H, d), _F32, at)
+    if out is not None:
+        _need(out, "out", shape, dt, at)
+    if dout is not None:
+        _need(dout, "dout", shape, dt, at)
     return B, H, L, d, ldg
 
 
@@ -278,20 +299,22 @@ def norm_gate(o, gate, weight, eps: float, out=None, stream=None):
     divided by each row's root mean square, times weight ([d], or [H,d] for
     one per head; None: ones) and z/(1+exp(-z)) of gate [B,L,H*d] (rows; None:
     no gate).  Returns [B,L,H*d], the layout of the output projection."""
-    lib = load()
     B, H, L, d, ldg = check_norm_gate_shapes(o, gate, weight, out)
     eps = _eps(eps)
-    dev = o.device
-    with _on(dev, stream):
-        if out is None:
-            out = o.new_empty((B, L, H * d))
-        sb, sh, sl, _ = o.stride()
-        _check(lib.falcon_norm_gate(DTYPES[o.dtype], _p(o), sb, sh, sl, _p(gate), ldg, _p(weight),
-                                    int(weight is not None and weight.dim() == 2), eps, B, H, L, d, _p(out),
-                                    _raw_stream(dev.index)))
+    at = o.get_device()
+    if _elsewhere(at, stream):
+        with _on(o, stream):
+            return norm_gate(o, gate, weight, eps, out)
+    if out is None:
+        out = o.new_empty((B, L, H * d))
+    sb, sh, sl, _ = o.stride()
+    _check(load().falcon_norm_gate(DTYPES[o.dtype], o.data_ptr(), sb, sh, sl, _p(gate), ldg, _p(weight),
+                                   weight is not None and weight.dim() == 2, eps, B, H, L, d, out.data_ptr(),
+                                   _raw_stream(at)))
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def norm_gate_bwd_workspace_size(dtype, B: int, H: int, L: int, d: int) -> int:
     """falcon_norm_gate_bwd_workspace_size: device bytes of norm_gate_bwd's workspace."""
     n = ctypes.c_size_t(0)
@@ -306,28 +329,29 @@ def norm_gate_bwd(o, gate, weight, eps: float, dout, do=None, dgate=None, want_d
     dout, or written into `do` with its strides), dgate [B,L,H*d] (rows where
     given; None without a gate), dweight fp32 like weight (None without one,
     or with want_dweight=False)."""
-    lib = load()
-    B, H, L, d, ldg = check_norm_gate_shapes(o, gate, weight, None, dout, do, dgate)
-    if gate is None and dgate is not None:
-        raise FalconError("dgate without a gate")
+    B, H, L, d, ldg = check_norm_gate_shapes(o, gate, weight, None, dout, do)
+    at = o.get_device()
+    lddg = H * d
+    if dgate is not None:
+        if gate is None:
+            raise FalconError("dgate without a gate")
+        lddg = _rows(dgate, "dgate", (B, L, H * d), o.dtype, at)
     eps = _eps(eps)
-    dev = o.device
-    with _on(dev, stream):
-        lddg = H * d
-        if do is None:
-            do = o.new_empty((B, H, L, d))
-        if dgate is not None:
-            lddg = _rows(dgate, "dgate", (B, L, H * d), o.dtype, dev)
-        elif gate is not None:
-            dgate = o.new_empty((B, L, H * d))
-        dweight = torch.empty_like(weight) if weight is not None and want_dweight else None
-        ws, have = _workspace(norm_gate_bwd_workspace_size(o.dtype, B, H, L, d), workspace, dev)
-        sb, sh, sl, _ = o.stride()
-        tb, th, tl, _ = do.stride()
-        _check(lib.falcon_norm_gate_bwd_ws(DTYPES[o.dtype], _p(o), sb, sh, sl, _p(gate), ldg, _p(weight),
-                                           int(weight is not None and weight.dim() == 2), eps, B, H, L, d, _p(dout),
-                                           _p(do), tb, th, tl, _p(dgate), lddg, _p(dweight), _p(ws), have,
-                                           _raw_stream(dev.index)))
+    if _elsewhere(at, stream):
+        with _on(o, stream):
+            return norm_gate_bwd(o, gate, weight, eps, dout, do, dgate, want_dweight, None, workspace)
+    if do is None:
+        do = o.new_empty((B, H, L, d))
+    if dgate is None and gate is not None:
+        dgate = o.new_empty((B, L, H * d))
+    dweight = torch.empty_like(weight) if weight is not None and want_dweight else None
+    ws, have = _workspace(norm_gate_bwd_workspace_size(o.dtype, B, H, L, d), workspace, o)
+    sb, sh, sl, _ = o.stride()
+    tb, th, tl, _ = do.stride()
+    _check(load().falcon_norm_gate_bwd_ws(DTYPES[o.dtype], o.data_ptr(), sb, sh, sl, _p(gate), ldg, _p(weight),
+                                          weight is not None and weight.dim() == 2, eps, B, H, L, d, dout.data_ptr(),
+                                          do.data_ptr(), tb, th, tl, _p(dgate), lddg, _p(dweight), _p(ws), have,
+                                          _raw_stream(at)))
     return {"do": do, "dgate": dgate, "dweight": dweight}
 
 
@@ -340,18 +364,22 @@ def check_residual_norm_shapes(r, weight, y=None, scale=None, **like_r):
     if r.dim() < 1:
         _shape_error("r must be [..., D]")
     _dtype(r, "r")
-    shape, dev = r.shape, r.device
+    shape, dt, at = r.shape, r.dtype, r.get_device()
     D = shape[-1]
     if not 1 <= D <= NORM_MAX_D:
         _shape_error("the rows must have 1 to %d channels, got %d" % (NORM_MAX_D, D))
-    _need(r, "r", shape, r.dtype, dev)
-    _need(y, "y", shape, r.dtype, dev)
+    _need(r, "r", shape, dt, at)
+    if y is not None:
+        _need(y, "y", shape, dt, at)
     for name, t in like_r.items():
-        _need(t, name, shape, r.dtype, dev)
-    _need(scale, "scale", (D,), torch.float32, dev)
-    _need(weight, "weight", (D,), torch.float32, dev)
-    if scale is not None and y is None:
-        raise FalconError("a scale without what it scales (y)")
+        if t is not None:
+            _need(t, name, shape, dt, at)
+    if scale is not None:
+        if y is None:
+            raise FalconError("a scale without what it scales (y)")
+        _need(scale, "scale", (D,), _F32, at)
+    if weight is not None:
+        _need(weight, "weight", (D,), _F32, at)
     return r.numel() // D, D
 
 
@@ -360,23 +388,25 @@ def residual_norm(r, weight, eps: float, y=None, scale=None, r_out=None, h=None,
     y, and that divided by its root mean square, times weight [D].  Returns
     (r_out, h); r_out may be `r` itself (the stream updated in place), and is
     `r` where there is no y."""
-    lib = load()
     R, D = check_residual_norm_shapes(r, weight, y, scale, r_out=r_out, h=h)
     eps = _eps(eps)
     if h is not None and r_out is not None and h.data_ptr() == r_out.data_ptr() and R:
         raise FalconError("h and r_out are the same array")
-    dev = r.device
-    with _on(dev, stream):
-        if h is None:
-            h = torch.empty_like(r)
-        write = r_out
-        if y is not None and r_out is None:
-            write = torch.empty_like(r)
-        _check(lib.falcon_residual_norm(DTYPES[r.dtype], _p(r), _p(y), _p(scale), _p(weight), eps, R, D, _p(write),
-                                        _p(h), _raw_stream(dev.index)))
+    at = r.get_device()
+    if _elsewhere(at, stream):
+        with _on(r, stream):
+            return residual_norm(r, weight, eps, y, scale, r_out, h)
+    if h is None:
+        h = torch.empty_like(r)
+    write = r_out
+    if y is not None and r_out is None:
+        write = torch.empty_like(r)
+    _check(load().falcon_residual_norm(DTYPES[r.dtype], r.data_ptr(), _p(y), _p(scale), _p(weight), eps, R, D,
+                                       _p(write), h.data_ptr(), _raw_stream(at)))
     return (r if write is None else write), h
 
 
+@functools.lru_cache(maxsize=4096)
 def residual_norm_bwd_workspace_size(dtype, R: int, D: int) -> int:
     """falcon_residual_norm_bwd_workspace_size: device bytes of residual_norm_bwd's workspace."""
     n = ctypes.c_size_t(0)
@@ -391,24 +421,25 @@ def residual_norm_bwd(r_out, weight, eps: float, dh, dr_out=None, y=None, scale=
     reads the stream; None: zero).  Returns a dict: dr (of r), dy (of y; the
     same tensor as dr without a scale; None without y), dscale, dweight fp32
     (None without scale, weight).  dr may be dr_out or dh."""
-    lib = load()
     R, D = check_residual_norm_shapes(r_out, weight, y, scale, dh=dh, dr_out=dr_out, dr=dr, dy=dy)
     eps = _eps(eps)
     if dy is not None and scale is None:
         raise FalconError("without a scale dy is dr: it is not written apart")
     if dr is not None and dy is not None and dr.data_ptr() == dy.data_ptr() and R:
         raise FalconError("dr and dy are the same array")
-    dev = r_out.device
-    with _on(dev, stream):
-        if dr is None:
-            dr = torch.empty_like(r_out)
-        if dy is None and scale is not None:
-            dy = torch.empty_like(r_out)
-        dscale = None if scale is None else torch.empty_like(scale)
-        dweight = None if weight is None else torch.empty_like(weight)
-        ws, have = _workspace(residual_norm_bwd_workspace_size(r_out.dtype, R, D), workspace, dev)
-        _check(lib.falcon_residual_norm_bwd_ws(DTYPES[r_out.dtype], _p(r_out), _p(y), _p(scale), _p(weight), _p(dh),
-                                               _p(dr_out), eps, R, D, _p(dr), _p(dy), _p(dscale), _p(dweight),
-                                               _p(ws), have, _raw_stream(dev.index)))
+    at = r_out.get_device()
+    if _elsewhere(at, stream):
+        with _on(r_out, stream):
+            return residual_norm_bwd(r_out, weight, eps, dh, dr_out, y, scale, dr, dy, None, workspace)
+    if dr is None:
+        dr = torch.empty_like(r_out)
+    if dy is None and scale is not None:
+        dy = torch.empty_like(r_out)
+    dscale = None if scale is None else torch.empty_like(scale)
+    dweight = None if weight is None else torch.empty_like(weight)
+    ws, have = _workspace(residual_norm_bwd_workspace_size(r_out.dtype, R, D), workspace, r_out)
+    _check(load().falcon_residual_norm_bwd_ws(DTYPES[r_out.dtype], r_out.data_ptr(), _p(y), _p(scale), _p(weight),
+                                              dh.data_ptr(), _p(dr_out), eps, R, D, dr.data_ptr(), _p(dy), _p(dscale),
+                                              _p(dweight), _p(ws), have, _raw_stream(at)))
     return {"dr": dr, "dy": dy if scale is not None else (dr if y is not None else None), "dscale": dscale,
             "dweight": dweight}
