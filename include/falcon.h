@@ -459,7 +459,8 @@ int falcon_decode_carry_from_prefill_ex(falcon_variant variant, falcon_dtype dty
  *            begins at n*L*stride): values and forget gates.  f = +inf keeps
  *            the state as it is (x finite); from f = -80 downwards less than
  *            2^-114 of it is left.
- *            L is at most 2^30, N*ceil(D/32) at most 2^26.
+ *            L is at most 2^30, N*ceil(D/32) at most 2^26, D and every row
+ *            stride (of a tensor of more than one row) at most 2^21.
  *   reset    [N,L] bytes, or NULL: where non-zero, token t begins a new
  *            document in a packed sequence and what came before does not
  *            reach it, whatever its value (infinities and NaN included)
@@ -619,7 +620,8 @@ int falcon_fwd_masked_noalloc(falcon_variant variant, falcon_dtype dtype,
 /*
  * falcon_device_wait_timeouts -- diagnostic: how many thread blocks of the
  * tensor-core kernels on the current device gave up on a bounded wait for
- * their own tensor-core work (about 2 s per wait) since the library was
+ * their own tensor-core work (about 2 s per wait), or of falcon_scan's kernels
+ * on one for the other blocks of their cluster, since the library was
  * loaded (each wait gives up after 4e9 SM cycles, 2-4 s).  A block that
  * gives up skips its remaining chunks, frees its tensor
  * memory and exits, so the device stays usable; its outputs are then

@@ -52,6 +52,13 @@ bool scan_sizes_ok(int N, int L, int D) {
     return items <= kMaxItems / 32;
 }
 
+// a row stride of the recurrence: the kernels place a tile's elements (at most
+// 512 tokens) by 32-bit byte offsets
+constexpr long long kScanMaxStride = 1 << 21;
+bool scan_stride_ok(long long ld, long long rows, long long D) {
+    return D <= kScanMaxStride && stride_ok(ld, rows, D) && (rows <= 1 || ld <= kScanMaxStride);
+}
+
 size_t marks_floats(int N, int L, int D) { return (size_t)N * ((L + kScanBlock - 1) / kScanBlock) * D; }
 
 }  // namespace
@@ -61,13 +68,13 @@ extern "C" int falcon_scan(falcon_dtype dtype, const void *x, const void *f, con
                            void *out, float *final_state, float *marks, cudaStream_t stream) {
     if (!dtype_ok(dtype)) return FALCON_ERR_ENUM;
     const long long rows = (long long)N * L;
-    if (!scan_sizes_ok(N, L, D) || !stride_ok(x_stride, rows, D) || !stride_ok(f_stride, rows, D))
+    if (!scan_sizes_ok(N, L, D) || !scan_stride_ok(x_stride, rows, D) || !scan_stride_ok(f_stride, rows, D))
         return FALCON_ERR_SHAPE;
     if (N == 0 || D == 0) return FALCON_OK;
     if (L == 0) return fill_f32(final_state, initial_state, (size_t)N * D, stream);
     if (!x || !f || !out) return FALCON_ERR_NULL;
     ScanParams p{};
-    p.N = N; p.L = L; p.D = D; p.ldx = x_stride; p.ldf = f_stride;
+    p.N = N; p.L = L; p.D = D; p.ldx = rows > 1 ? x_stride : D; p.ldf = rows > 1 ? f_stride : D;
     p.x = x; p.f = f; p.reset = reset; p.init_state = initial_state;
     p.out = out; p.final_state = final_state; p.marks = marks;
     return done(dtype == FALCON_BF16 ? launch_scan<__nv_bfloat16>(p, stream) : launch_scan<float>(p, stream));
@@ -90,8 +97,8 @@ extern "C" int falcon_scan_bwd_ws(falcon_dtype dtype, const void *x, const void 
                                   void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (!dtype_ok(dtype)) return FALCON_ERR_ENUM;
     const long long rows = (long long)N * L;
-    if (!scan_sizes_ok(N, L, D) || !stride_ok(x_stride, rows, D) || !stride_ok(f_stride, rows, D) ||
-        !stride_ok(dx_stride, rows, D) || !stride_ok(df_stride, rows, D))
+    if (!scan_sizes_ok(N, L, D) || !scan_stride_ok(x_stride, rows, D) || !scan_stride_ok(f_stride, rows, D) ||
+        !scan_stride_ok(dx_stride, rows, D) || !scan_stride_ok(df_stride, rows, D))
         return FALCON_ERR_SHAPE;
     if (N == 0 || D == 0) return FALCON_OK;
     if (L == 0) return fill_f32(dinitial, dstate, (size_t)N * D, stream);
@@ -100,7 +107,7 @@ extern "C" int falcon_scan_bwd_ws(falcon_dtype dtype, const void *x, const void 
     if (!marks) {
         if (!ws_ok(workspace, workspace_bytes, marks_floats(N, L, D) * sizeof(float))) return FALCON_ERR_WORKSPACE;
         ScanParams q{};
-        q.N = N; q.L = L; q.D = D; q.ldx = x_stride; q.ldf = f_stride;
+        q.N = N; q.L = L; q.D = D; q.ldx = rows > 1 ? x_stride : D; q.ldf = rows > 1 ? f_stride : D;
         q.x = x; q.f = f; q.reset = reset; q.init_state = initial_state;
         q.marks = static_cast<float *>(workspace);
         const int rc = done(bf16 ? launch_scan<__nv_bfloat16>(q, stream) : launch_scan<float>(q, stream));
@@ -108,7 +115,9 @@ extern "C" int falcon_scan_bwd_ws(falcon_dtype dtype, const void *x, const void 
         marks = q.marks;
     }
     ScanBwdParams p{};
-    p.N = N; p.L = L; p.D = D; p.ldx = x_stride; p.ldf = f_stride; p.lddx = dx_stride; p.lddf = df_stride;
+    p.N = N; p.L = L; p.D = D;
+    const bool one = rows <= 1;  // no second row: the strides say nothing
+    p.ldx = one ? D : x_stride; p.ldf = one ? D : f_stride; p.lddx = one ? D : dx_stride; p.lddf = one ? D : df_stride;
     p.x = x; p.f = f; p.reset = reset; p.marks = marks; p.dout = dout; p.dstate = dstate;
     p.dx = dx; p.df = df; p.dinitial = dinitial;
     return done(bf16 ? launch_scan_bwd<__nv_bfloat16>(p, stream) : launch_scan_bwd<float>(p, stream));

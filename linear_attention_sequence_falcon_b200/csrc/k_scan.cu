@@ -10,10 +10,12 @@
 // tile of runs, and a cluster of blocks takes neighbouring tiles at once and
 // walks the sequence.  Each thread forms its run's map from registers; the
 // maps of the tile are joined through shared memory, those of the cluster's
-// tiles through distributed shared memory, one cluster barrier per step; then
-// the thread applies its map to the state that enters its run and writes.
-// Every input is read once.  The order of all joins is fixed by the token's
-// position alone, so results do not depend on the cluster's size.
+// tiles through distributed shared memory: every block sends its tile's map to
+// all of its cluster (st.async, counted by the receiver's mbarrier, so that no
+// store to global memory has to be waited for, as a cluster barrier's release
+// would); then the thread applies its map to the state that enters its run and
+// writes.  Every input is read once.  The order of all joins is fixed by the
+// token's position alone, so results do not depend on the cluster's size.
 //
 // The backward pass walks the other way with the same products A:
 //   g_t = dout_t + y_t,  y_{t-1} = (reset_t ? 0 : a_t g_t),
@@ -30,15 +32,17 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "params_layer.h"
+#include "tc_sm100.cuh"
 
 namespace falcon {
 
 namespace {
 
-constexpr int kRun = 8;        // tokens per run
 constexpr int kThreads = 256;  // 8 warps per block
 constexpr int kMaxCluster = 8;
-static_assert(kScanBlock == 8 * kRun, "a mark in front of every eighth run");
+constexpr uint64_t kGiveUpNs = 2000000000ull;  // a wait for the cluster's maps
+
+__device__ unsigned int g_scan_wait_timeouts;
 
 // ---- pairs of fp32 in one instruction
 __device__ __forceinline__ unsigned long long bits(float2 v) { return *reinterpret_cast<unsigned long long *>(&v); }
@@ -173,83 +177,177 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// writes v at `p` of this block's shared memory in the shared memory of `rank`
-__device__ __forceinline__ void store_remote(const float4 *p, uint32_t rank, float4 v) {
+__device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank) {
     uint32_t to;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(tc::smem_u32(p)), "r"(rank));
+    return to;
+}
+// v to the place of `p`, in the shared memory of `rank`, counted by its `bar`
+__device__ __forceinline__ void send(const float4 *p, const uint64_t *bar, uint32_t rank, float4 v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                     remote(p, rank)),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(remote(bar, rank))
                  : "memory");
 }
+__device__ __forceinline__ bool wait_parity(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 
-// Which of the run's kRun tokens begin a document, as bits; the LPR lanes of
+// The exchange of the tiles' maps inside a cluster.  Step s uses half s & 1 of
+// `maps`: a block sends step s + 2 only after every block's map of step s + 1
+// has come, which each sends after its reads of step s.
+template <int LPR> struct Cluster {
+    float4 maps[2][kMaxCluster][LPR];
+    uint64_t bar[2];
+    int gave_up;
+
+    __device__ __forceinline__ void begin(int cs) {
+        if (threadIdx.x == 0) {
+            gave_up = 0;
+            tc::mbar_init(&bar[0], 1);
+            tc::mbar_init(&bar[1], 1);
+            tc::fence_mbar_init();
+        }
+        if (cs > 1) {  // no block writes to another before that runs and its barriers stand
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        }
+    }
+    // the maps of turn `turn` (0, 1, ...) have come; false: given up
+    __device__ __forceinline__ bool wait(int turn) {
+        uint64_t *b = &bar[turn & 1];
+        const uint32_t parity = (turn >> 1) & 1;
+        if (wait_parity(b, parity)) return true;
+        const long long t0 = clock64();
+        while (!wait_parity(b, parity))
+            if (clock64() - t0 > (long long)(2 * kGiveUpNs)) {
+                gave_up = 1;
+                return false;
+            }
+        return true;
+    }
+    // no block leaves while another may still write to it
+    __device__ __forceinline__ void end(int cs) {
+        if (cs == 1) return;
+        __syncthreads();
+        if (threadIdx.x == 0 && gave_up) atomicAdd(&g_scan_wait_timeouts, 1u);
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    }
+};
+
+// Which of the run's RUN tokens begin a document, as bits; the LPR lanes of
 // a run look at its bytes together.
-template <int LPR>
+template <int LPR, int RUN>
 __device__ __forceinline__ uint32_t reset_bits(const unsigned char *reset, long long row, int left, int lane) {
     const int l = lane % LPR, base = lane - l;
     uint32_t got = 0;
 #pragma unroll
-    for (int i = 0; i < kRun; i += LPR) {
+    for (int i = 0; i < RUN; i += LPR) {
         const int t = i + l;
-        const bool set = t < kRun && t < left && reset[row + t] != 0;
+        const bool set = t < RUN && t < left && reset[row + t] != 0;
         got |= ((__ballot_sync(0xffffffffu, set) >> base) & (LPR >= 32 ? 0xffffffffu : (1u << LPR) - 1u)) << i;
     }
-    return got & ((1u << kRun) - 1u);
+    return got & ((1u << RUN) - 1u);
 }
 
-// The place of a thread: LPR lanes, a pair of channels each, per run; 32/LPR
-// runs per warp.
-template <int LPR> struct Place {
+// The place of a thread: LPR lanes, a pair of channels each, per run of RUN
+// tokens; 32/LPR runs per warp.
+template <int LPR, int RUN> struct Place {
     static constexpr int kChannels = 2 * LPR;
     static constexpr int kRuns = kThreads / LPR;      // per tile
-    static constexpr int kTile = kRuns * kRun;        // tokens
+    static constexpr int kTile = kRuns * RUN;         // tokens
+    static constexpr int kMark = kScanBlock / RUN;    // runs between two marks
+};
+
+constexpr int kRun = 8;  // tokens of a run
+
+// One array's rows as a thread meets them.  Inside a tile that is whole (all
+// tokens, all channels) an element is at a 32-bit offset from the tile's first
+// byte: the strides are at most 2^21 elements, a tile is at most 512 tokens.
+template <typename T, bool V, int RUN> struct Rows {
+    const char *base;   // the sequence's first token, channel 0
+    long long ld;       // bytes from token to token
+    uint32_t off;       // this thread's first token and channel, in a tile
+    __device__ __forceinline__ Rows(const void *p, long long elements, long long stride, int u, int ch)
+        : base(static_cast<const char *>(p) + elements * (long long)sizeof(T)),
+          ld(stride * (long long)sizeof(T)),
+          off((uint32_t)(u * RUN) * (uint32_t)ld + (uint32_t)(ch * (int)sizeof(T))) {}
+    template <bool WHOLE>
+    __device__ __forceinline__ Raw<T> load(long long tile0, int i, int gap, bool in0, bool in1, float fill) const {
+        const T *p = reinterpret_cast<const T *>(base + tile0 * ld + (off + (uint32_t)i * (uint32_t)ld));
+        if constexpr (WHOLE) return load_pair<T, V>(p, gap, true, true, fill);
+        else return load_pair<T, V>(p, gap, in0, in1, fill);
+    }
+    template <bool WHOLE>
+    __device__ __forceinline__ void store(long long tile0, int i, int gap, bool in0, bool in1, float2 v) const {
+        T *p = reinterpret_cast<T *>(const_cast<char *>(base) + tile0 * ld + (off + (uint32_t)i * (uint32_t)ld));
+        if constexpr (WHOLE) store_pair<T, V>(p, gap, true, true, v);
+        else store_pair<T, V>(p, gap, in0, in1, v);
+    }
 };
 
 template <typename T, bool V, int LPR, bool R>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) scan_kernel(ScanParams p) {
-    using G = Place<LPR>;
+    constexpr int RUN = kRun;
+    using G = Place<LPR, RUN>;
     __shared__ float4 agg[2][kThreads];
-    __shared__ float4 cl[2][kMaxCluster][LPR];
+    __shared__ Cluster<LPR> cl;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, u = threadIdx.x / LPR;
     const int cs = (int)cluster_size(), rank = (int)cluster_rank();
-    if (cs > 1) cluster_arrive();
+    cl.begin(cs);
     const int groups = (p.D + G::kChannels - 1) / G::kChannels;
     const int unit_id = blockIdx.x / cs, n = unit_id / groups;
-    const int ch = (unit_id % groups) * G::kChannels + (V ? 2 * l : l);
+    const int ch0 = (unit_id % groups) * G::kChannels, ch = ch0 + (V ? 2 * l : l);
     constexpr int gap = LPR;
-    const bool in0 = ch < p.D, in1 = V ? in0 : ch + gap < p.D;
+    const bool in0 = ch < p.D, in1 = V ? in0 : ch + gap < p.D, wide = ch0 + G::kChannels <= p.D;
     const int nblk = (p.L + kScanBlock - 1) / kScanBlock;
     const int tiles = (p.L + G::kTile - 1) / G::kTile, steps = (tiles + cs - 1) / cs;
-    const T *x = static_cast<const T *>(p.x) + (long long)n * p.L * p.ldx + ch;
-    const T *f = static_cast<const T *>(p.f) + (long long)n * p.L * p.ldf + ch;
-    T *out = p.out ? static_cast<T *>(p.out) + (long long)n * p.L * p.D + ch : nullptr;
+    const Rows<T, V, RUN> x(p.x, (long long)n * p.L * p.ldx, p.ldx, u, ch);
+    const Rows<T, V, RUN> f(p.f, (long long)n * p.L * p.ldf, p.ldf, u, ch);
+    const Rows<T, V, RUN> out(p.out, (long long)n * p.L * p.D, p.D, u, ch);
     const float *init = p.init_state ? p.init_state + (long long)n * p.D + ch : nullptr;
 
     float2 carry = make_float2(init && in0 ? init[0] : 0.f, init && in1 ? init[V ? 1 : gap] : 0.f);
-    Raw<T> rx[kRun], rf[kRun];
+    Raw<T> rx[RUN], rf[RUN];
     uint32_t rr = 0;
     auto fetch = [&](int step) {
-        const int t0 = (step * cs + rank) * G::kTile + u * kRun;
         if (step >= steps) return;
-        if constexpr (R) rr = reset_bits<LPR>(p.reset, (long long)n * p.L + t0, p.L - t0, lane);
+        const int tile0 = (step * cs + rank) * G::kTile, t0 = tile0 + u * RUN;
+        if constexpr (R) rr = reset_bits<LPR, RUN>(p.reset, (long long)n * p.L + t0, p.L - t0, lane);
+        if (wide && tile0 + G::kTile <= p.L) {
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            // tokens behind the end keep the state: f = +inf
-            const bool in = t0 + i < p.L;
-            rx[i] = load_pair<T, V>(x + (t0 + i) * p.ldx, gap, in && in0, in && in1, 0.f);
-            rf[i] = load_pair<T, V>(f + (t0 + i) * p.ldf, gap, in && in0, in && in1, __int_as_float(0x7f800000));
+            for (int i = 0; i < RUN; ++i) {
+                rx[i] = x.template load<true>(tile0, i, gap, true, true, 0.f);
+                rf[i] = f.template load<true>(tile0, i, gap, true, true, 0.f);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {  // tokens behind the end keep the state: f = +inf
+                const bool in = t0 + i < p.L;
+                rx[i] = x.template load<false>(tile0, i, gap, in && in0, in && in1, 0.f);
+                rf[i] = f.template load<false>(tile0, i, gap, in && in0, in && in1, __int_as_float(0x7f800000));
+            }
         }
     };
     fetch(0);
     for (int step = 0; step < steps; ++step) {
-        const int t0 = (step * cs + rank) * G::kTile + u * kRun, par = step & 1;
+        const int tile0 = (step * cs + rank) * G::kTile, t0 = tile0 + u * RUN, par = step & 1;
+        if (cs > 1 && threadIdx.x == 0) tc::mbar_arrive_expect_tx(&cl.bar[par], cs * LPR * sizeof(float4));
         // the run from a zero state: pa = product of the gates up to here, hl = the state
-        float2 pa[kRun], hl[kRun];
+        float2 pa[RUN], hl[RUN];
         const uint32_t cut = rr;
-        const int first = R && cut ? __ffs(cut) - 1 : kRun;
+        const int first = R && cut ? __ffs(cut) - 1 : RUN;
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
+        for (int i = 0; i < RUN; ++i) {
             float2 a, c;
             gates(rf[i].f(), a, c);
             const float2 b = mul2(c, rx[i].f());
@@ -258,106 +356,121 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) scan_kernel(
             pa[i] = i == 0 ? a : mul2(a, pa[i - 1]);
             if (R && i >= first) pa[i] = make_float2(-0.f, -0.f);
         }
-        agg[par][threadIdx.x] = as4({pa[kRun - 1], hl[kRun - 1]});
+        agg[par][threadIdx.x] = as4({pa[RUN - 1], hl[RUN - 1]});
         fetch(step + 1);
         __syncthreads();
-        // the map in front of this run, and the tile's
-        Map before = unit(), all = unit();
-#pragma unroll 8
-        for (int i = 0; i < G::kRuns; ++i) {
-            if (i == u) before = all;
-            all = join<R>(load_map(&agg[par][i * LPR + l]), all);
-        }
+        if (cs > 1 && cl.gave_up) break;
+        // the map in front of this run, and, for those who pass it on, the tile's
+        Map before = unit();
+        for (int i = 0; i < u; ++i) before = join<R>(load_map(&agg[par][i * LPR + l]), before);
         float2 h = carry;
+        if (cs == 1 || warp < cs) {
+            Map all = before;
+            for (int i = u; i < G::kRuns; ++i) all = join<R>(load_map(&agg[par][i * LPR + l]), all);
+            if (cs == 1) carry = apply<R>(all, h);
+            else if (lane < LPR) send(&cl.maps[par][rank][l], &cl.bar[par], warp, as4(all));
+        }
         if (cs > 1) {
-            if (step == 0) cluster_wait();  // every block of the cluster runs before its memory is written
-            if (warp < cs && lane < LPR) store_remote(&cl[par][rank][l], warp, as4(all));
-            __syncwarp();
-            cluster_arrive();
-            cluster_wait();
+            cl.wait(step);
             float2 mine = h;
             for (int i = 0; i < cs; ++i) {
                 if (i == rank) mine = h;
-                h = apply<R>(load_map(&cl[par][i][l]), h);
+                h = apply<R>(load_map(&cl.maps[par][i][l]), h);
             }
             carry = h;
             h = mine;
-        } else {
-            carry = apply<R>(all, h);
         }
         h = apply<R>(before, h);
-        if (p.marks && u % 8 == 0 && t0 < p.L)
+        if (p.marks && u % G::kMark == 0 && t0 < p.L)
             store_pair<float, false>(p.marks + ((long long)n * nblk + t0 / kScanBlock) * p.D + ch, V ? 1 : gap, in0,
                                      in1, h);
-        if (out) {
+        if (!p.out) continue;
+        if (wide && tile0 + G::kTile <= p.L) {
 #pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                const float2 v = R && i >= first ? hl[i] : fma2(pa[i], h, hl[i]);
-                if (t0 + i < p.L) store_pair<T, V>(out + (long long)(t0 + i) * p.D, gap, in0, in1, v);
+            for (int i = 0; i < RUN; ++i)
+                out.template store<true>(tile0, i, gap, true, true, R && i >= first ? hl[i] : fma2(pa[i], h, hl[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                const bool in = t0 + i < p.L;
+                out.template store<false>(tile0, i, gap, in && in0, in && in1,
+                                          R && i >= first ? hl[i] : fma2(pa[i], h, hl[i]));
             }
         }
     }
     if (p.final_state && rank == 0 && threadIdx.x < LPR)
         store_pair<float, false>(p.final_state + (long long)n * p.D + ch, V ? 1 : gap, in0, in1, carry);
+    cl.end(cs);
 }
 
 template <typename T, bool V, int LPR, bool R>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanBwdParams p) {
-    using G = Place<LPR>;
-    constexpr bool kAhead = sizeof(T) == 2;  // the next tile's loads before this one's barriers (fp32: no registers)
+    constexpr int RUN = kRun;
+    using G = Place<LPR, RUN>;
+    constexpr bool kAhead = sizeof(T) == 2;  // the next tile's loads before this one's joins (fp32: no registers)
     __shared__ float4 agg[2][kThreads];      // product of the gates, y's map
     __shared__ float2 fwd[2][kThreads];      // the state's B
-    __shared__ float4 cl[2][kMaxCluster][LPR];
+    __shared__ Cluster<LPR> cl;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, u = threadIdx.x / LPR;
     const int cs = (int)cluster_size(), rank = (int)cluster_rank();
-    if (cs > 1) cluster_arrive();
+    cl.begin(cs);
     const int groups = (p.D + G::kChannels - 1) / G::kChannels;
     const int unit_id = blockIdx.x / cs, n = unit_id / groups;
-    const int ch = (unit_id % groups) * G::kChannels + (V ? 2 * l : l);
+    const int ch0 = (unit_id % groups) * G::kChannels, ch = ch0 + (V ? 2 * l : l);
     constexpr int gap = LPR;
-    const bool in0 = ch < p.D, in1 = V ? in0 : ch + gap < p.D;
+    const bool in0 = ch < p.D, in1 = V ? in0 : ch + gap < p.D, wide = ch0 + G::kChannels <= p.D;
     const int nblk = (p.L + kScanBlock - 1) / kScanBlock;
     const int tiles = (p.L + G::kTile - 1) / G::kTile, steps = (tiles + cs - 1) / cs;
-    const T *x = static_cast<const T *>(p.x) + (long long)n * p.L * p.ldx + ch;
-    const T *f = static_cast<const T *>(p.f) + (long long)n * p.L * p.ldf + ch;
-    const T *dout = static_cast<const T *>(p.dout) + (long long)n * p.L * p.D + ch;
-    T *dx = static_cast<T *>(p.dx) + (long long)n * p.L * p.lddx + ch;
-    T *df = static_cast<T *>(p.df) + (long long)n * p.L * p.lddf + ch;
+    const Rows<T, V, RUN> x(p.x, (long long)n * p.L * p.ldx, p.ldx, u, ch);
+    const Rows<T, V, RUN> f(p.f, (long long)n * p.L * p.ldf, p.ldf, u, ch);
+    const Rows<T, V, RUN> dout(p.dout, (long long)n * p.L * p.D, p.D, u, ch);
+    const Rows<T, V, RUN> dx(p.dx, (long long)n * p.L * p.lddx, p.lddx, u, ch);
+    const Rows<T, V, RUN> df(p.df, (long long)n * p.L * p.lddf, p.lddf, u, ch);
     const float *ds = p.dstate ? p.dstate + (long long)n * p.D + ch : nullptr;
 
     float2 carry = make_float2(ds && in0 ? ds[0] : 0.f, ds && in1 ? ds[V ? 1 : gap] : 0.f);
-    Raw<T> rx[kRun], rf[kRun], rd[kRun];
+    Raw<T> rx[RUN], rf[RUN], rd[RUN];
     float2 rm = make_float2(0.f, 0.f);
     uint32_t rr = 0;
     auto fetch = [&](int step) {  // steps from the last tokens to the first
         if (step < 0) return;
-        const int t0 = (step * cs + rank) * G::kTile + u * kRun;
-        if constexpr (R) rr = reset_bits<LPR>(p.reset, (long long)n * p.L + t0, p.L - t0, lane);
+        const int tile0 = (step * cs + rank) * G::kTile, t0 = tile0 + u * RUN;
+        if constexpr (R) rr = reset_bits<LPR, RUN>(p.reset, (long long)n * p.L + t0, p.L - t0, lane);
         const Raw<float> m = load_pair<float, false>(
             p.marks + ((long long)n * nblk + t0 / kScanBlock) * p.D + ch, V ? 1 : gap, t0 < p.L && in0,
             t0 < p.L && in1, 0.f);
         rm = m.v;
+        if (wide && tile0 + G::kTile <= p.L) {
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            // tokens behind the end hand y on: f = +inf, dout = 0
-            const bool in = t0 + i < p.L;
-            rx[i] = load_pair<T, V>(x + (t0 + i) * p.ldx, gap, in && in0, in && in1, 0.f);
-            rf[i] = load_pair<T, V>(f + (t0 + i) * p.ldf, gap, in && in0, in && in1, __int_as_float(0x7f800000));
-            rd[i] = load_pair<T, V>(dout + (long long)(t0 + i) * p.D, gap, in && in0, in && in1, 0.f);
+            for (int i = 0; i < RUN; ++i) {
+                rx[i] = x.template load<true>(tile0, i, gap, true, true, 0.f);
+                rf[i] = f.template load<true>(tile0, i, gap, true, true, 0.f);
+                rd[i] = dout.template load<true>(tile0, i, gap, true, true, 0.f);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {  // tokens behind the end hand y on: f = +inf, dout = 0
+                const bool in = t0 + i < p.L;
+                rx[i] = x.template load<false>(tile0, i, gap, in && in0, in && in1, 0.f);
+                rf[i] = f.template load<false>(tile0, i, gap, in && in0, in && in1, __int_as_float(0x7f800000));
+                rd[i] = dout.template load<false>(tile0, i, gap, in && in0, in && in1, 0.f);
+            }
         }
     };
     if constexpr (kAhead) fetch(steps - 1);
     for (int step = steps - 1; step >= 0; --step) {
-        const int t0 = (step * cs + rank) * G::kTile + u * kRun, par = step & 1;
+        const int turn = steps - 1 - step, par = turn & 1;
+        const int tile0 = (step * cs + rank) * G::kTile, t0 = tile0 + u * RUN;
+        if (cs > 1 && threadIdx.x == 0) tc::mbar_arrive_expect_tx(&cl.bar[par], cs * LPR * sizeof(float4));
         if constexpr (!kAhead) fetch(step);
         const uint32_t cut = rr;
-        const int first = R && cut ? __ffs(cut) - 1 : kRun;
+        const int first = R && cut ? __ffs(cut) - 1 : RUN;
         const float2 mark = rm;
-        float2 a[kRun], c[kRun], q[kRun];  // q: c x, later a c (h - x)
-        Raw<T> dy[kRun];
+        float2 a[RUN], c[RUN], q[RUN];  // q: c x, later a c (h - x)
+        Raw<T> dy[RUN];
         float2 pa, hl, yl = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
+        for (int i = 0; i < RUN; ++i) {
             gates(rf[i].f(), a[i], c[i]);
             q[i] = mul2(c[i], rx[i].f());
             dy[i] = rd[i];
@@ -371,61 +484,60 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanBwdParams p) 
         fwd[par][threadIdx.x] = hl;
         if constexpr (kAhead) fetch(step - 1);
         __syncthreads();
+        if (cs > 1 && cl.gave_up) break;
+        // y's map behind this run, and, for those who pass it on, the tile's
+        Map behind = unit();
+        for (int i = G::kRuns - 1; i > u; --i) behind = join<R>(load_map(&agg[par][i * LPR + l]), behind);
+        float2 y = carry;
+        if (cs == 1 || warp < cs) {
+            Map all = behind;
+            for (int i = u; i >= 0; --i) all = join<R>(load_map(&agg[par][i * LPR + l]), all);
+            if (cs == 1) carry = apply<R>(all, y);
+            else if (lane < LPR) send(&cl.maps[par][rank][l], &cl.bar[par], warp, as4(all));
+        }
         // the state in front of this run, from the mark of its eight
         float2 h = mark;
-        const int u0 = u & ~7;
+        for (int i = u & ~(G::kMark - 1); i < u; ++i) {
+            const Map m = load_map(&agg[par][i * LPR + l]);
+            h = apply<R>({m.a, fwd[par][i * LPR + l]}, h);
+        }
 #pragma unroll
-        for (int i = 0; i < 7; ++i) {
-            if (u0 + i < u) {
-                const Map m = load_map(&agg[par][(u0 + i) * LPR + l]);
-                h = apply<R>({m.a, fwd[par][(u0 + i) * LPR + l]}, h);
-            }
-        }
-        // y's map behind this run, and the tile's
-        Map behind = unit(), all = unit();
-#pragma unroll 8
-        for (int i = G::kRuns - 1; i >= 0; --i) {
-            if (i == u) behind = all;
-            all = join<R>(load_map(&agg[par][i * LPR + l]), all);
-        }
-        float2 y = carry;
-        if (cs > 1) {
-            if (step == steps - 1) cluster_wait();  // every block of the cluster runs before its memory is written
-            if (warp < cs && lane < LPR) store_remote(&cl[par][rank][l], warp, as4(all));
-            __syncwarp();
-            cluster_arrive();
-            cluster_wait();
-            float2 mine = y;
-            for (int i = cs - 1; i >= 0; --i) {
-                if (i == rank) mine = y;
-                y = apply<R>(load_map(&cl[par][i][l]), y);
-            }
-            carry = y;
-            y = mine;
-        } else {
-            carry = apply<R>(all, y);
-        }
-        y = apply<R>(behind, y);
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
+        for (int i = 0; i < RUN; ++i) {
             const bool r = R && (cut >> i & 1);
             const float2 hp = r ? make_float2(0.f, 0.f) : h;
             const float2 b = q[i];
             q[i] = mul2(a[i], fma2(c[i], hp, make_float2(-b.x, -b.y)));
             h = r ? b : fma2(a[i], h, b);
         }
+        if (cs > 1) {
+            cl.wait(turn);
+            float2 mine = y;
+            for (int i = cs - 1; i >= 0; --i) {
+                if (i == rank) mine = y;
+                y = apply<R>(load_map(&cl.maps[par][i][l]), y);
+            }
+            carry = y;
+            y = mine;
+        }
+        y = apply<R>(behind, y);
+        const bool whole = wide && tile0 + G::kTile <= p.L;
 #pragma unroll
-        for (int i = kRun - 1; i >= 0; --i) {
+        for (int i = RUN - 1; i >= 0; --i) {
             const float2 g = add2(dy[i].f(), y);
-            if (t0 + i < p.L) {
-                store_pair<T, V>(dx + (t0 + i) * p.lddx, gap, in0, in1, mul2(g, c[i]));
-                store_pair<T, V>(df + (t0 + i) * p.lddf, gap, in0, in1, mul2(g, q[i]));
+            if (whole) {
+                dx.template store<true>(tile0, i, gap, true, true, mul2(g, c[i]));
+                df.template store<true>(tile0, i, gap, true, true, mul2(g, q[i]));
+            } else {
+                const bool in = t0 + i < p.L;
+                dx.template store<false>(tile0, i, gap, in && in0, in && in1, mul2(g, c[i]));
+                df.template store<false>(tile0, i, gap, in && in0, in && in1, mul2(g, q[i]));
             }
             y = R && (cut >> i & 1) ? make_float2(0.f, 0.f) : mul2(a[i], g);
         }
     }
     if (p.dinitial && rank == 0 && threadIdx.x < LPR)
         store_pair<float, false>(p.dinitial + (long long)n * p.D + ch, V ? 1 : gap, in0, in1, carry);
+    cl.end(cs);
 }
 
 template <typename T, bool V>
@@ -533,7 +645,7 @@ template <typename T> int launch_scan(const ScanParams &p, cudaStream_t s) {
     const bool v = p.D % 2 == 0 && pair_aligned(p.x, sizeof(T), p.ldx) && pair_aligned(p.f, sizeof(T), p.ldf) &&
                    (!p.out || pair_aligned(p.out, sizeof(T), p.D));
     return with_lanes(p.D, [&](auto lpr) {
-        using G = Place<decltype(lpr)::value>;
+        using G = Place<decltype(lpr)::value, kRun>;
         const long long units = (long long)p.N * ((p.D + G::kChannels - 1) / G::kChannels);
         return with_bools(v, p.reset != nullptr, [&](auto vv, auto rr) {
             return launch_units(scan_kernel<T, decltype(vv)::value, decltype(lpr)::value, decltype(rr)::value>, p,
@@ -547,7 +659,7 @@ template <typename T> int launch_scan_bwd(const ScanBwdParams &p, cudaStream_t s
                    pair_aligned(p.dout, sizeof(T), p.D) && pair_aligned(p.dx, sizeof(T), p.lddx) &&
                    pair_aligned(p.df, sizeof(T), p.lddf);
     return with_lanes(p.D, [&](auto lpr) {
-        using G = Place<decltype(lpr)::value>;
+        using G = Place<decltype(lpr)::value, kRun>;
         const long long units = (long long)p.N * ((p.D + G::kChannels - 1) / G::kChannels);
         return with_bools(v, p.reset != nullptr, [&](auto vv, auto rr) {
             return launch_units(scan_bwd_kernel<T, decltype(vv)::value, decltype(lpr)::value, decltype(rr)::value>, p,
@@ -564,6 +676,12 @@ template <typename T> int launch_scan_step(const ScanStepParams &p, cudaStream_t
     if (v) scan_step_kernel<T, true><<<blocks, 128, 0, s>>>(p);
     else scan_step_kernel<T, false><<<blocks, 128, 0, s>>>(p);
     return 0;
+}
+
+unsigned int scan_wait_timeouts() {
+    unsigned int v = 0;
+    cudaMemcpyFromSymbol(&v, g_scan_wait_timeouts, sizeof(v));
+    return v;
 }
 
 template int launch_scan<float>(const ScanParams &, cudaStream_t);

@@ -27,6 +27,8 @@ def test_scan_codes(lib):
     assert _scan(lib, N=-1) == SHAPE and _scan(lib, L=-1) == SHAPE and _scan(lib, D=-1) == SHAPE
     assert _scan(lib, ldx=63) == SHAPE and _scan(lib, ldf=0) == SHAPE
     assert _scan(lib, ldx=1 << 60) == SHAPE                       # offsets beyond 63 bits
+    assert _scan(lib, ldx=(1 << 21) + 1) == SHAPE and _scan(lib, N=1, L=1, D=(1 << 21) + 1) == SHAPE
+    assert _scan(lib, L=(1 << 30) + 1) == SHAPE
     assert _scan(lib, N=2 ** 30, D=4096, ldx=4096, ldf=4096) == SHAPE
     assert _scan(lib, x=None) == NULL and _scan(lib, f=None) == NULL and _scan(lib, out=None) == NULL
     assert _scan(lib, N=0) == OK and _scan(lib, D=0) == OK and _scan(lib, L=0, x=None, f=None, out=None) == OK
