@@ -26,238 +26,17 @@
 // A map that contains a reset ignores what comes before, infinities and NaN
 // included: its A is -0.0 (no product of gates is), and it is applied by
 // selection, not by multiplication.
-#include <mutex>
-#include <type_traits>
-
-#include "common.cuh"
-#include "kernels.h"
-#include "params_layer.h"
-#include "tc_sm100.cuh"
+#include "scan_parts.cuh"
 
 namespace falcon {
+
+using namespace scan;
 
 namespace {
 
 constexpr int kThreads = 256;  // 8 warps per block
-constexpr int kMaxCluster = 8;
-constexpr uint64_t kGiveUpNs = 2000000000ull;  // a wait for the cluster's maps
 
 __device__ unsigned int g_scan_wait_timeouts;
-
-// ---- pairs of fp32 in one instruction
-__device__ __forceinline__ unsigned long long bits(float2 v) { return *reinterpret_cast<unsigned long long *>(&v); }
-__device__ __forceinline__ float2 pair(unsigned long long v) { return *reinterpret_cast<float2 *>(&v); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-    return pair(d);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-    return pair(d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-    return pair(d);
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
-
-// a = sigmoid(f), c = 1 - a, each to full relative accuracy, without a branch
-// on f's sign: e = exp(-f), a = 1/(1+e), c = e a.  The exponent is held at
-// 115 (f = -79.7: a is 2e-35 from there on), so that e a stays finite.
-__device__ __forceinline__ void gates(float2 f, float2 &a, float2 &c) {
-    const float2 z = mul2(f, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-    const float2 e = make_float2(ex2(min_nan(z.x, 115.f)), ex2(min_nan(z.y, 115.f)));
-    const float2 s = add2(e, make_float2(1.f, 1.f));
-    a = make_float2(rcp(s.x), rcp(s.y));
-    c = mul2(e, a);
-}
-
-// ---- loads and stores of one thread's two channels (V: next to each other
-// and aligned as a pair; otherwise `gap` apart, each by itself)
-template <typename T> struct Raw;
-template <> struct Raw<float> {
-    float2 v;
-    __device__ __forceinline__ float2 f() const { return v; }
-    __device__ __forceinline__ void set(float x, float y) { v = make_float2(x, y); }
-};
-template <> struct Raw<__nv_bfloat16> {
-    uint32_t v;
-    __device__ __forceinline__ float2 f() const {
-        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-    }
-    __device__ __forceinline__ void set(float x, float y) {  // values bf16 holds exactly
-        v = (__float_as_uint(x) >> 16) | (__float_as_uint(y) & 0xffff0000u);
-    }
-};
-
-template <typename T, bool V>
-__device__ __forceinline__ Raw<T> load_pair(const T *p, int gap, bool in0, bool in1, float fill) {
-    Raw<T> r;
-    r.set(fill, fill);
-    if constexpr (V) {
-        if (in0) r.v = *reinterpret_cast<const decltype(r.v) *>(p);
-    } else {
-        const float x = in0 ? to_f32(p[0]) : fill, y = in1 ? to_f32(p[gap]) : fill;
-        r.set(x, y);
-    }
-    return r;
-}
-
-template <typename T, bool V>
-__device__ __forceinline__ void store_pair(T *p, int gap, bool in0, bool in1, float2 v) {
-    if constexpr (V) {
-        if (!in0) return;
-        if constexpr (sizeof(T) == 2)
-            *reinterpret_cast<__nv_bfloat162 *>(p) = __float22bfloat162_rn(v);
-        else
-            *reinterpret_cast<float2 *>(p) = v;
-    } else {
-        if (in0) p[0] = from_f32<T>(v.x);
-        if (in1) p[gap] = from_f32<T>(v.y);
-    }
-}
-
-// ---- affine maps of a pair of channels
-struct Map {
-    float2 a, b;
-};
-__device__ __forceinline__ bool cuts(float a) { return __float_as_uint(a) == 0x80000000u; }
-// m applied to h (R: m may contain a reset)
-template <bool R> __device__ __forceinline__ float2 apply(const Map &m, float2 h) {
-    float2 v = fma2(m.a, h, m.b);
-    if constexpr (R) {
-        if (cuts(m.a.x)) v.x = m.b.x;
-        if (cuts(m.a.y)) v.y = m.b.y;
-    }
-    return v;
-}
-// `after` behind `before`, as one map
-template <bool R> __device__ __forceinline__ Map join(const Map &after, const Map &before) {
-    Map m;
-    m.b = apply<R>(after, before.b);
-    m.a = mul2(after.a, before.a);
-    if constexpr (R) {
-        if (cuts(after.a.x)) m.a.x = after.a.x;
-        if (cuts(after.a.y)) m.a.y = after.a.y;
-    }
-    return m;
-}
-__device__ __forceinline__ Map unit() { return {make_float2(1.f, 1.f), make_float2(0.f, 0.f)}; }
-
-__device__ __forceinline__ Map load_map(const float4 *p) {
-    const float4 v = *p;
-    return {make_float2(v.x, v.y), make_float2(v.z, v.w)};
-}
-__device__ __forceinline__ float4 as4(const Map &m) { return make_float4(m.a.x, m.a.y, m.b.x, m.b.y); }
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank) {
-    uint32_t to;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(tc::smem_u32(p)), "r"(rank));
-    return to;
-}
-// v to the place of `p`, in the shared memory of `rank`, counted by its `bar`
-__device__ __forceinline__ void send(const float4 *p, const uint64_t *bar, uint32_t rank, float4 v) {
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-                     remote(p, rank)),
-                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(remote(bar, rank))
-                 : "memory");
-}
-__device__ __forceinline__ bool wait_parity(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(tc::smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// The exchange of the tiles' maps inside a cluster.  Step s uses half s & 1 of
-// `maps`: a block sends step s + 2 only after every block's map of step s + 1
-// has come, which each sends after its reads of step s.
-template <int LPR> struct Cluster {
-    float4 maps[2][kMaxCluster][LPR];
-    uint64_t bar[2];
-    int gave_up;
-
-    __device__ __forceinline__ void begin(int cs) {
-        if (threadIdx.x == 0) {
-            gave_up = 0;
-            tc::mbar_init(&bar[0], 1);
-            tc::mbar_init(&bar[1], 1);
-            tc::fence_mbar_init();
-        }
-        if (cs > 1) {  // no block writes to another before that runs and its barriers stand
-            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        }
-    }
-    // the maps of turn `turn` (0, 1, ...) have come; false: given up
-    __device__ __forceinline__ bool wait(int turn) {
-        uint64_t *b = &bar[turn & 1];
-        const uint32_t parity = (turn >> 1) & 1;
-        if (wait_parity(b, parity)) return true;
-        const long long t0 = clock64();
-        while (!wait_parity(b, parity))
-            if (clock64() - t0 > (long long)(2 * kGiveUpNs)) {
-                gave_up = 1;
-                return false;
-            }
-        return true;
-    }
-    // no block leaves while another may still write to it
-    __device__ __forceinline__ void end(int cs) {
-        if (cs == 1) return;
-        __syncthreads();
-        if (threadIdx.x == 0 && gave_up) atomicAdd(&g_scan_wait_timeouts, 1u);
-        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    }
-};
-
-// Which of the run's RUN tokens begin a document, as bits; the LPR lanes of
-// a run look at its bytes together.
-template <int LPR, int RUN>
-__device__ __forceinline__ uint32_t reset_bits(const unsigned char *reset, long long row, int left, int lane) {
-    const int l = lane % LPR, base = lane - l;
-    uint32_t got = 0;
-#pragma unroll
-    for (int i = 0; i < RUN; i += LPR) {
-        const int t = i + l;
-        const bool set = t < RUN && t < left && reset[row + t] != 0;
-        got |= ((__ballot_sync(0xffffffffu, set) >> base) & (LPR >= 32 ? 0xffffffffu : (1u << LPR) - 1u)) << i;
-    }
-    return got & ((1u << RUN) - 1u);
-}
 
 // The place of a thread: LPR lanes, a pair of channels each, per run of RUN
 // tokens; 32/LPR runs per warp.
@@ -400,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) scan_kernel(
     }
     if (p.final_state && rank == 0 && threadIdx.x < LPR)
         store_pair<float, false>(p.final_state + (long long)n * p.D + ch, V ? 1 : gap, in0, in1, carry);
-    cl.end(cs);
+    cl.end(cs, &g_scan_wait_timeouts);
 }
 
 template <typename T, bool V, int LPR, bool R>
@@ -537,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanBwdParams p) 
     }
     if (p.dinitial && rank == 0 && threadIdx.x < LPR)
         store_pair<float, false>(p.dinitial + (long long)n * p.D + ch, V ? 1 : gap, in0, in1, carry);
-    cl.end(cs);
+    cl.end(cs, &g_scan_wait_timeouts);
 }
 
 template <typename T, bool V>
@@ -560,72 +339,6 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanStepParams p) {
 
 // ---- launches
 
-bool pair_aligned(const void *p, size_t elt, long long ld) {
-    return (reinterpret_cast<uintptr_t>(p) & (2 * elt - 1)) == 0 && ld % 2 == 0;
-}
-
-// How many clusters of `cs` blocks of a kernel the device holds at once, from
-// the occupancy calculator, kept per (kernel, device, cs).
-template <typename K> int clusters_held(K kernel, int cs) {
-    constexpr int kDevices = 16;
-    static std::mutex guard;
-    static struct { const void *k; int held[kDevices][kMaxCluster + 1]; } kept[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 148 * 2 / cs;
-    std::lock_guard<std::mutex> lock(guard);
-    int *slot = nullptr;
-    for (auto &e : kept) {
-        if (e.k == nullptr) e.k = reinterpret_cast<const void *>(kernel);
-        if (e.k == reinterpret_cast<const void *>(kernel)) { slot = &e.held[dev][cs]; break; }
-    }
-    if (slot && *slot) return *slot;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3(cs * 148);
-    c.blockDim = dim3(kThreads);
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = cs; at.val.clusterDim.y = 1; at.val.clusterDim.z = 1;
-    c.attrs = &at;
-    c.numAttrs = 1;
-    int held = 0;
-    if (cudaOccupancyMaxActiveClusters(&held, kernel, &c) != cudaSuccess || held < 1) {
-        cudaGetLastError();
-        held = 1;
-    }
-    if (slot) *slot = held;
-    return held;
-}
-
-// The cluster's size: blocks walk steps = tiles/cs tiles each, in as many
-// waves as the device needs for all units' clusters; the size with the least
-// waves x steps, the smallest of equals (a smaller cluster joins fewer maps).
-template <typename K> int pick_cluster(K kernel, long long units, int tiles) {
-    int best = 1;
-    long long cost = 0;
-    for (int cs = 1; cs <= kMaxCluster && cs <= tiles; ++cs) {
-        const long long waves = (units + clusters_held(kernel, cs) - 1) / clusters_held(kernel, cs);
-        const long long here = waves * ((tiles + cs - 1) / cs);
-        if (cs == 1 || here < cost) { best = cs; cost = here; }
-    }
-    return best;
-}
-
-template <typename K, typename P> int launch_units(K kernel, const P &p, long long units, int tiles, cudaStream_t s) {
-    const int cs = pick_cluster(kernel, units, tiles);
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)(units * cs));
-    c.blockDim = dim3(kThreads);
-    c.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = cs; at.val.clusterDim.y = 1; at.val.clusterDim.z = 1;
-    c.attrs = &at;
-    c.numAttrs = cs > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&c, kernel, p) == cudaSuccess) return 0;
-    cudaGetLastError();
-    return -7;
-}
-
 // Lanes per run: the fewest that hold the row's pairs, 32 at most.
 template <typename F> int with_lanes(int D, F go) {
     if (D <= 8) return go(std::integral_constant<int, 4>());
@@ -642,19 +355,23 @@ template <typename F> int with_bools(bool v, bool r, F go) {
 }  // namespace
 
 template <typename T> int launch_scan(const ScanParams &p, cudaStream_t s) {
+    const int tma = launch_scan_tma<T>(p, s);
+    if (tma != 1) return tma;
     const bool v = p.D % 2 == 0 && pair_aligned(p.x, sizeof(T), p.ldx) && pair_aligned(p.f, sizeof(T), p.ldf) &&
                    (!p.out || pair_aligned(p.out, sizeof(T), p.D));
     return with_lanes(p.D, [&](auto lpr) {
         using G = Place<decltype(lpr)::value, kRun>;
         const long long units = (long long)p.N * ((p.D + G::kChannels - 1) / G::kChannels);
         return with_bools(v, p.reset != nullptr, [&](auto vv, auto rr) {
-            return launch_units(scan_kernel<T, decltype(vv)::value, decltype(lpr)::value, decltype(rr)::value>, p,
-                                units, (p.L + G::kTile - 1) / G::kTile, s);
+            return launch_units(scan_kernel<T, decltype(vv)::value, decltype(lpr)::value, decltype(rr)::value>,
+                                units, (p.L + G::kTile - 1) / G::kTile, kThreads, 0, s, p);
         });
     });
 }
 
 template <typename T> int launch_scan_bwd(const ScanBwdParams &p, cudaStream_t s) {
+    const int tma = launch_scan_bwd_tma<T>(p, s);
+    if (tma != 1) return tma;
     const bool v = p.D % 2 == 0 && pair_aligned(p.x, sizeof(T), p.ldx) && pair_aligned(p.f, sizeof(T), p.ldf) &&
                    pair_aligned(p.dout, sizeof(T), p.D) && pair_aligned(p.dx, sizeof(T), p.lddx) &&
                    pair_aligned(p.df, sizeof(T), p.lddf);
@@ -662,8 +379,8 @@ template <typename T> int launch_scan_bwd(const ScanBwdParams &p, cudaStream_t s
         using G = Place<decltype(lpr)::value, kRun>;
         const long long units = (long long)p.N * ((p.D + G::kChannels - 1) / G::kChannels);
         return with_bools(v, p.reset != nullptr, [&](auto vv, auto rr) {
-            return launch_units(scan_bwd_kernel<T, decltype(vv)::value, decltype(lpr)::value, decltype(rr)::value>, p,
-                                units, (p.L + G::kTile - 1) / G::kTile, s);
+            return launch_units(scan_bwd_kernel<T, decltype(vv)::value, decltype(lpr)::value, decltype(rr)::value>,
+                                units, (p.L + G::kTile - 1) / G::kTile, kThreads, 0, s, p);
         });
     });
 }
@@ -681,7 +398,7 @@ template <typename T> int launch_scan_step(const ScanStepParams &p, cudaStream_t
 unsigned int scan_wait_timeouts() {
     unsigned int v = 0;
     cudaMemcpyFromSymbol(&v, g_scan_wait_timeouts, sizeof(v));
-    return v;
+    return v + scan_tma_wait_timeouts();
 }
 
 template int launch_scan<float>(const ScanParams &, cudaStream_t);
