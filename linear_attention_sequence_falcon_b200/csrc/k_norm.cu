@@ -38,8 +38,8 @@ __device__ __forceinline__ float inv_rms(float ms, float eps) {
 // 1/(1+exp(-z)), to 0 for a far negative z
 __device__ __forceinline__ float sigmoid(float z) {
     float e, s;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
     return s;
 }
 

@@ -151,13 +151,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) scan_kernel(
         }
         if (cs > 1) {
             cl.wait(step);
-            float2 mine = h;
-            for (int i = 0; i < cs; ++i) {
-                if (i == rank) mine = h;
-                h = apply<R>(load_map(&cl.maps[par][i][l]), h);
-            }
+            for (int i = 0; i < rank; ++i) h = apply<R>(load_map(&cl.maps[par][i][l]), h);
             carry = h;
-            h = mine;
+            for (int i = rank; i < cs; ++i) carry = apply<R>(load_map(&cl.maps[par][i][l]), carry);
         }
         h = apply<R>(before, h);
         if (p.marks && u % G::kMark == 0 && t0 < p.L)
@@ -290,13 +286,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanBwdParams p) 
         }
         if (cs > 1) {
             cl.wait(turn);
-            float2 mine = y;
-            for (int i = cs - 1; i >= 0; --i) {
-                if (i == rank) mine = y;
-                y = apply<R>(load_map(&cl.maps[par][i][l]), y);
-            }
+            for (int i = cs - 1; i > rank; --i) y = apply<R>(load_map(&cl.maps[par][i][l]), y);
             carry = y;
-            y = mine;
+            for (int i = rank; i >= 0; --i) carry = apply<R>(load_map(&cl.maps[par][i][l]), carry);
         }
         y = apply<R>(behind, y);
         const bool whole = wide && tile0 + G::kTile <= p.L;
