@@ -13,8 +13,14 @@
 // thread keeps its channels from row to row: the weights stay in registers
 // and their gradients are added up there, over the rows that the thread
 // meets, then over the block's rows through shared memory, then over the
-// blocks by sum_parts_kernel.  All orders are fixed by the sizes.  The next
-// row's loads are issued before the present row's sums are joined.
+// blocks by sum_parts_kernel.  All orders are fixed by the sizes.
+//
+// The bound is HBM: what it takes is bytes in flight.  A thread keeps the next
+// two rows' pieces on their way as asynchronous copies into its own places
+// of shared memory (no other thread reads them, so no barrier is needed, and
+// no registers are held).
+#include <atomic>
+#include <initializer_list>
 #include <type_traits>
 
 #include "common.cuh"
@@ -28,6 +34,7 @@ namespace {
 constexpr int kSms = 148;
 constexpr int kMinRows = 4;     // rows that a block walks at least, where weights' gradients are wanted
 constexpr int kSegments = 8;    // partial sums joined side by side
+constexpr int kMaxRows = 3;     // rows of a thread in shared memory: the present one and two on their way
 
 // 1/sqrt(ms + eps); a row of zeros with eps = 0 is left as zeros
 __device__ __forceinline__ float inv_rms(float ms, float eps) {
@@ -43,31 +50,27 @@ __device__ __forceinline__ float sigmoid(float z) {
     return s;
 }
 
-// ---- a thread's share of a row: NC places of VEC channels, as stored
+// ---- VEC neighbouring channels, as stored
 template <typename T, int VEC> struct Piece;
 template <> struct Piece<__nv_bfloat16, 8> { uint4 v; };
-template <> struct Piece<float, 4> { uint4 v; };
+template <> struct Piece<__nv_bfloat16, 2> { uint32_t v; };
 template <> struct Piece<__nv_bfloat16, 1> { unsigned short v; };
-template <> struct Piece<float, 1> { float v; };
+template <> struct Piece<float, 4> { uint4 v; };
+template <> struct Piece<float, 1> { uint32_t v; };
 
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ void widen(const Piece<__nv_bfloat16, 8> &p, float *f) {
-    const uint32_t w[4] = {p.v.x, p.v.y, p.v.z, p.v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    f[0] = low(p.v.x), f[1] = high(p.v.x), f[2] = low(p.v.y), f[3] = high(p.v.y);
+    f[4] = low(p.v.z), f[5] = high(p.v.z), f[6] = low(p.v.w), f[7] = high(p.v.w);
 }
+__device__ __forceinline__ void widen(const Piece<__nv_bfloat16, 2> &p, float *f) { f[0] = low(p.v), f[1] = high(p.v); }
+__device__ __forceinline__ void widen(const Piece<__nv_bfloat16, 1> &p, float *f) { f[0] = low(p.v); }
 __device__ __forceinline__ void widen(const Piece<float, 4> &p, float *f) {
-    f[0] = __uint_as_float(p.v.x);
-    f[1] = __uint_as_float(p.v.y);
-    f[2] = __uint_as_float(p.v.z);
-    f[3] = __uint_as_float(p.v.w);
+    f[0] = __uint_as_float(p.v.x), f[1] = __uint_as_float(p.v.y);
+    f[2] = __uint_as_float(p.v.z), f[3] = __uint_as_float(p.v.w);
 }
-__device__ __forceinline__ void widen(const Piece<__nv_bfloat16, 1> &p, float *f) {
-    f[0] = __uint_as_float((uint32_t)p.v << 16);
-}
-__device__ __forceinline__ void widen(const Piece<float, 1> &p, float *f) { f[0] = p.v; }
+__device__ __forceinline__ void widen(const Piece<float, 1> &p, float *f) { f[0] = __uint_as_float(p.v); }
 
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
@@ -76,30 +79,78 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 __device__ __forceinline__ void narrow(Piece<__nv_bfloat16, 8> &p, const float *f) {
     p.v = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
-__device__ __forceinline__ void narrow(Piece<float, 4> &p, const float *f) {
-    p.v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-}
+__device__ __forceinline__ void narrow(Piece<__nv_bfloat16, 2> &p, const float *f) { p.v = pack2(f[0], f[1]); }
 __device__ __forceinline__ void narrow(Piece<__nv_bfloat16, 1> &p, const float *f) {
     p.v = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
 }
-__device__ __forceinline__ void narrow(Piece<float, 1> &p, const float *f) { p.v = f[0]; }
+__device__ __forceinline__ void narrow(Piece<float, 4> &p, const float *f) {
+    p.v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ void narrow(Piece<float, 1> &p, const float *f) { p.v = __float_as_uint(f[0]); }
 
-template <typename T, int VEC, int NC> struct Share {
+// ---- a thread's pieces of the present row and of those to come, A arrays each:
+// S rows in shared memory (three where they fit the block's, whatever fits
+// otherwise), S - 1 of them on their way.  Two-byte pieces have no
+// asynchronous copy and the widest fp32 rows no room: S = 0, read when used.
+template <typename T, int VEC, int NC, int A, int MT> struct Ahead {
     using P = Piece<T, VEC>;
-    P p[NC];
-    __device__ __forceinline__ void load(const T *row, int t, int tpr, int d, bool ok) {
+    static constexpr int kRow = A * NC * (int)sizeof(P);  // bytes per thread
+    static constexpr int kFit = 200 * 1024 / (MT * kRow);
+    static constexpr int S = sizeof(P) == 2 ? 0 : kFit < kMaxRows ? kFit : kMaxRows;
+    static constexpr int kAhead = S > 0 ? S - 1 : 0;
+    static constexpr int kBytes = S * kRow;
+    P *mine;
+    int t, tpr, d, threads;
+    const T *at[S == 0 ? A : 1];  // S = 0: the present row
+
+    __device__ __forceinline__ Ahead(uint8_t *smem, int t_, int tpr_, int d_)
+        : mine(reinterpret_cast<P *>(smem) + threadIdx.x), t(t_), tpr(tpr_), d(d_), threads(blockDim.x) {}
+    __device__ __forceinline__ P *place(int stage, int a, int j) const {
+        return mine + ((stage * A + a) * NC + j) * threads;
+    }
+    // array a of a row (zeros where not ok, and behind the row's end)
+    __device__ __forceinline__ void fetch(int stage, int a, const T *row, bool ok) {
+        if constexpr (S == 0) {
+            at[a] = ok ? row : nullptr;
+        } else {
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            const int c = (j * tpr + t) * VEC;
-            p[j].v = {};
-            if (ok && c < d) p[j] = *reinterpret_cast<const P *>(row + c);
+            for (int j = 0; j < NC; ++j) {
+                const int c = (j * tpr + t) * VEC;
+                const bool in = ok && c < d;
+                const uint32_t dst = (uint32_t)__cvta_generic_to_shared(place(stage, a, j));
+                const T *src = in ? row + c : row;
+                const int bytes = in ? (int)sizeof(P) : 0;
+                if constexpr (sizeof(P) == 16)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+                else
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+            }
         }
     }
-    __device__ __forceinline__ void get(float *f) const {
-#pragma unroll
-        for (int j = 0; j < NC; ++j) widen(p[j], f + j * VEC);
+    static __device__ __forceinline__ void close() {
+        if constexpr (S > 0) asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    static __device__ __forceinline__ void store(T *row, int t, int tpr, int d, const float *f) {
+    // all but the last kAhead rows' copies have come
+    static __device__ __forceinline__ void wait() {
+        if constexpr (S > 0) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+    }
+    static __device__ __forceinline__ void wait_all() {
+        if constexpr (S > 0) asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    __device__ __forceinline__ void get(int stage, int a, float *f) const {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            if constexpr (S == 0) {
+                const int c = (j * tpr + t) * VEC;
+                P v{};
+                if (at[a] && c < d) v = *reinterpret_cast<const P *>(at[a] + c);
+                widen(v, f + j * VEC);
+            } else {
+                widen(*place(stage, a, j), f + j * VEC);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T *row, const float *f) const {
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
             const int c = (j * tpr + t) * VEC;
@@ -108,6 +159,9 @@ template <typename T, int VEC, int NC> struct Share {
             if (c < d) *reinterpret_cast<P *>(row + c) = q;
         }
     }
+    // the stage behind the present one's last copy, and the next present one
+    static __device__ __forceinline__ int last(int stage) { return S <= 1 ? 0 : stage == 0 ? S - 1 : stage - 1; }
+    static __device__ __forceinline__ int next(int stage) { return S <= 1 || stage == S - 1 ? 0 : stage + 1; }
 };
 
 // a thread's channels of an fp32 vector (NULL: ones); 0 behind the row's end
@@ -223,83 +277,104 @@ struct GateWalk {
     }
 };
 
+// Blocks per SM that the registers have to leave room for: threads up to 256,
+// 512 (16 channels each) and 1024 (rows beyond 8192).
+constexpr int fwd_blocks(int mt) { return mt == 256 ? 4 : 1; }
+constexpr int bwd_blocks(int mt) { return mt == 256 ? 3 : 1; }
+
 template <typename T, int VEC, int NC, int MT, bool GATE>
-__global__ void __launch_bounds__(MT, MT == 256 ? 4 : 1) norm_gate_kernel(NormGateParams p, int tpr, int parts) {
+__global__ void __launch_bounds__(MT, fwd_blocks(MT)) norm_gate_kernel(NormGateParams p, int tpr, int parts) {
     constexpr int E = VEC * NC;
-    using S = Share<T, VEC, NC>;
+    using Rows = Ahead<T, VEC, NC, GATE ? 2 : 1, MT>;
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][32][2];
     const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, d = p.d;
-    GateRows r;
-    GateWalk w;
+    Rows rows(smem, t, tpr, d);
+    GateRows r, next;
+    GateWalk w, ahead;
     w.begin(p, parts, slots, slot, r);
+    ahead = w;
+    next = r;
+    auto fetch = [&](int stage) {
+        const bool ok = ahead.row < ahead.rows;
+        if (ok) gate_offsets(p, next, ahead.h0 + next.h);
+        else next.o = next.g = 0;
+        rows.fetch(stage, 0, static_cast<const T *>(p.o) + next.o, ok);
+        if constexpr (GATE) rows.fetch(stage, 1, static_cast<const T *>(p.gate) + next.g, ok);
+        rows.close();
+        ahead.next(p, next);
+    };
+    for (int i = 0; i < Rows::kAhead; ++i) fetch(i);
     float wt[E];
     load_weights<VEC, NC>(wt, p.weight ? p.weight + (long long)w.h0 * d : nullptr, t, tpr, d);
-    S o, z;
-    auto fetch = [&]() {
-        const bool ok = w.row < w.rows;
-        if (ok) gate_offsets(p, r, w.h0 + r.h);
-        o.load(static_cast<const T *>(p.o) + r.o, t, tpr, d, ok);
-        if constexpr (GATE) z.load(static_cast<const T *>(p.gate) + r.g, t, tpr, d, ok);
-    };
-    r.o = r.g = r.out = 0;
-    fetch();
     const long long first = (long long)(blockIdx.x % parts) * slots;
-    int parity = 0;
+    int parity = 0, stage = 0;
     for (long long base = first; base < w.rows; base += w.step, parity ^= 1) {
-        float ov[E], zv[E], sum[1] = {0.f};
-        o.get(ov);
-        if constexpr (GATE) z.get(zv);
+        fetch(Rows::last(stage));
+        rows.wait();
+        float ov[E], sum[1] = {0.f};
         const bool ok = w.row < w.rows;
-        T *out = static_cast<T *>(p.out) + r.out;
+        rows.get(stage, 0, ov);
 #pragma unroll
         for (int e = 0; e < E; ++e) sum[0] = fmaf(ov[e], ov[e], sum[0]);
-        w.next(p, r);
-        fetch();
         row_sum<1>(sum, tpr, slot, red, parity);
         const float rstd = inv_rms(sum[0] / d, p.eps);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            ov[e] *= rstd * wt[e];
-            if constexpr (GATE) ov[e] *= zv[e] * sigmoid(zv[e]);
+        for (int e = 0; e < E; ++e) ov[e] *= rstd * wt[e];
+        if constexpr (GATE) {
+            float zv[E];
+            rows.get(stage, 1, zv);
+#pragma unroll
+            for (int e = 0; e < E; ++e) ov[e] *= zv[e] * sigmoid(zv[e]);
         }
-        if (ok) S::store(out, t, tpr, d, ov);
+        if (ok) {
+            gate_offsets(p, r, w.h0 + r.h);
+            rows.store(static_cast<T *>(p.out) + r.out, ov);
+        }
+        w.next(p, r);
+        stage = Rows::next(stage);
     }
 }
 
 template <typename T, int VEC, int NC, int MT, bool GATE>
-__global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1) norm_gate_bwd_kernel(NormGateParams p, int tpr, int parts) {
+__global__ void __launch_bounds__(MT, bwd_blocks(MT)) norm_gate_bwd_kernel(NormGateParams p, int tpr, int parts) {
     constexpr int E = VEC * NC;
-    using S = Share<T, VEC, NC>;
+    using Rows = Ahead<T, VEC, NC, GATE ? 3 : 2, MT>;
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][32][2];
-    __shared__ float buf[MT == 256 ? 256 * E : 1];
     const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, d = p.d;
-    GateRows r;
-    GateWalk w;
+    Rows rows(smem, t, tpr, d);
+    GateRows r, next;
+    GateWalk w, ahead;
     w.begin(p, parts, slots, slot, r);
+    ahead = w;
+    next = r;
+    auto fetch = [&](int stage) {
+        const bool ok = ahead.row < ahead.rows;
+        if (ok) gate_offsets(p, next, ahead.h0 + next.h);
+        else next.o = next.out = next.g = 0;
+        rows.fetch(stage, 0, static_cast<const T *>(p.o) + next.o, ok);
+        rows.fetch(stage, 1, static_cast<const T *>(p.dout) + next.out, ok);
+        if constexpr (GATE) rows.fetch(stage, 2, static_cast<const T *>(p.gate) + next.g, ok);
+        rows.close();
+        ahead.next(p, next);
+    };
+    for (int i = 0; i < Rows::kAhead; ++i) fetch(i);
     float wt[E], dw[E];
     load_weights<VEC, NC>(wt, p.weight ? p.weight + (long long)w.h0 * d : nullptr, t, tpr, d);
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[e] = 0.f;
-    S o, z, g;
-    auto fetch = [&]() {
-        const bool ok = w.row < w.rows;
-        if (ok) gate_offsets(p, r, w.h0 + r.h);
-        o.load(static_cast<const T *>(p.o) + r.o, t, tpr, d, ok);
-        g.load(static_cast<const T *>(p.dout) + r.out, t, tpr, d, ok);
-        if constexpr (GATE) z.load(static_cast<const T *>(p.gate) + r.g, t, tpr, d, ok);
-    };
-    r.o = r.g = r.out = r.d_o = r.dg = 0;
-    fetch();
     const long long first = (long long)(blockIdx.x % parts) * slots;
     const float inv_d = 1.f / d;
-    int parity = 0;
+    int parity = 0, stage = 0;
     for (long long base = first; base < w.rows; base += w.step, parity ^= 1) {
+        fetch(Rows::last(stage));
+        rows.wait();
         float ov[E], zv[E], gv[E], sum[2] = {0.f, 0.f};
-        o.get(ov);
-        g.get(gv);
-        if constexpr (GATE) z.get(zv);
         const bool ok = w.row < w.rows;
-        T *d_o = static_cast<T *>(p.d_o) + r.d_o, *dgate = static_cast<T *>(p.dgate) + r.dg;
+        rows.get(stage, 0, ov);
+        rows.get(stage, 1, gv);
+        if constexpr (GATE) rows.get(stage, 2, zv);
         // gv: dout -> e = dout s(z); zv: z -> dout w s'(z) o, still without r
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -311,141 +386,149 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1) norm_gate_bwd_kernel(No
             sum[0] = fmaf(ov[e], ov[e], sum[0]);
             sum[1] = fmaf(gv[e] * wt[e], ov[e], sum[1]);
         }
-        w.next(p, r);
-        fetch();
         row_sum<2>(sum, tpr, slot, red, parity);
         const float rstd = inv_rms(sum[0] * inv_d, p.eps);
         const float m = sum[1] * inv_d * rstd * rstd;  // mean(e w n) r
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float n = ov[e] * rstd;
-            dw[e] = fmaf(gv[e], n, dw[e]);
+            dw[e] = fmaf(gv[e], ov[e] * rstd, dw[e]);
             ov[e] = fmaf(-ov[e], m, gv[e] * wt[e]) * rstd;
             if constexpr (GATE) zv[e] *= rstd;
         }
         if (ok) {
-            S::store(d_o, t, tpr, d, ov);
-            if constexpr (GATE) S::store(dgate, t, tpr, d, zv);
+            gate_offsets(p, r, w.h0 + r.h);
+            rows.store(static_cast<T *>(p.d_o) + r.d_o, ov);
+            if constexpr (GATE) rows.store(static_cast<T *>(p.dgate) + r.dg, zv);
         }
+        w.next(p, r);
+        stage = Rows::next(stage);
     }
+    Rows::wait_all();  // the block's sums take the copies' place
     if (p.dweight)
         block_part<VEC, NC>(dw, t, tpr, slot, slots, d,
-                            p.ws + ((long long)(blockIdx.x % parts) * (p.per_head ? p.H : 1) + w.h0) * d, buf);
+                            p.ws + ((long long)(blockIdx.x % parts) * (p.per_head ? p.H : 1) + w.h0) * d,
+                            reinterpret_cast<float *>(smem));
 }
 
 template <typename T, int VEC, int NC, int MT, bool ADD>
-__global__ void __launch_bounds__(MT, MT == 256 ? 4 : 1) residual_norm_kernel(ResidualNormParams p, int tpr) {
+__global__ void __launch_bounds__(MT, fwd_blocks(MT)) residual_norm_kernel(ResidualNormParams p, int tpr) {
     constexpr int E = VEC * NC;
-    using S = Share<T, VEC, NC>;
+    using Rows = Ahead<T, VEC, NC, ADD ? 2 : 1, MT>;
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][32][2];
     const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, d = p.D;
+    Rows rows(smem, t, tpr, d);
+    const long long step = (long long)gridDim.x * slots;
+    long long row = (long long)blockIdx.x * slots + slot, ahead = row;
+    auto fetch = [&](int stage) {
+        const bool ok = ahead < p.R;
+        const long long at = ok ? ahead * d : 0;
+        rows.fetch(stage, 0, static_cast<const T *>(p.r) + at, ok);
+        if constexpr (ADD) rows.fetch(stage, 1, static_cast<const T *>(p.y) + at, ok);
+        rows.close();
+        ahead += step;
+    };
+    for (int i = 0; i < Rows::kAhead; ++i) fetch(i);
     float wt[E], sc[E];
     load_weights<VEC, NC>(wt, p.weight, t, tpr, d);
     if constexpr (ADD) load_weights<VEC, NC>(sc, p.scale, t, tpr, d);
-    const int step = gridDim.x * slots;
-    long long row = (long long)blockIdx.x * slots + slot;
-    S a, b;
-    auto fetch = [&]() {
-        const long long at = row < p.R ? row * d : 0;
-        a.load(static_cast<const T *>(p.r) + at, t, tpr, d, row < p.R);
-        if constexpr (ADD) b.load(static_cast<const T *>(p.y) + at, t, tpr, d, row < p.R);
-    };
-    fetch();
-    int parity = 0;
+    int parity = 0, stage = 0;
     for (long long base = (long long)blockIdx.x * slots; base < p.R; base += step, parity ^= 1) {
-        float v[E], y[E], sum[1] = {0.f};
-        a.get(v);
-        if constexpr (ADD) b.get(y);
-        const bool ok = row < p.R;
-        const long long at = row * d;
+        fetch(Rows::last(stage));
+        rows.wait();
+        float v[E], sum[1] = {0.f};
+        rows.get(stage, 0, v);
+        if constexpr (ADD) {
+            float y[E];
+            rows.get(stage, 1, y);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            if constexpr (ADD) v[e] = fmaf(sc[e], y[e], v[e]);
-            sum[0] = fmaf(v[e], v[e], sum[0]);
+            for (int e = 0; e < E; ++e) v[e] = fmaf(sc[e], y[e], v[e]);
         }
-        row += step;
-        fetch();
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[0] = fmaf(v[e], v[e], sum[0]);
         row_sum<1>(sum, tpr, slot, red, parity);
         const float rstd = inv_rms(sum[0] / d, p.eps);
-        if (ok && p.r_out) S::store(static_cast<T *>(p.r_out) + at, t, tpr, d, v);
+        const bool ok = row < p.R;
+        if (ok && p.r_out) rows.store(static_cast<T *>(p.r_out) + row * d, v);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] *= rstd * wt[e];
-        if (ok) S::store(static_cast<T *>(p.h) + at, t, tpr, d, v);
+        if (ok) rows.store(static_cast<T *>(p.h) + row * d, v);
+        row += step;
+        stage = Rows::next(stage);
     }
 }
 
 template <typename T, int VEC, int NC, int MT, bool ADD>
-__global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1) residual_norm_bwd_kernel(ResidualNormParams p, int tpr) {
+__global__ void __launch_bounds__(MT, bwd_blocks(MT)) residual_norm_bwd_kernel(ResidualNormParams p, int tpr) {
     constexpr int E = VEC * NC;
-    using S = Share<T, VEC, NC>;
+    using Rows = Ahead<T, VEC, NC, ADD ? 4 : 3, MT>;
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][32][2];
-    __shared__ float buf[MT == 256 ? 256 * E : 1];
     const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, d = p.D;
+    Rows rows(smem, t, tpr, d);
+    const long long step = (long long)gridDim.x * slots;
+    long long row = (long long)blockIdx.x * slots + slot, ahead = row;
+    const bool stream = p.dr_out != nullptr;
+    auto fetch = [&](int stage) {
+        const bool ok = ahead < p.R;
+        const long long at = ok ? ahead * d : 0;
+        rows.fetch(stage, 0, static_cast<const T *>(p.r) + at, ok);
+        rows.fetch(stage, 1, static_cast<const T *>(p.dh) + at, ok);
+        rows.fetch(stage, 2, static_cast<const T *>(stream ? p.dr_out : p.dh) + at, ok && stream);
+        if constexpr (ADD) rows.fetch(stage, 3, static_cast<const T *>(p.y) + at, ok);
+        rows.close();
+        ahead += step;
+    };
+    for (int i = 0; i < Rows::kAhead; ++i) fetch(i);
     float wt[E], sc[E], dw[E], ds[E];
     load_weights<VEC, NC>(wt, p.weight, t, tpr, d);
     load_weights<VEC, NC>(sc, p.scale, t, tpr, d);
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[e] = ds[e] = 0.f;
-    const int step = gridDim.x * slots;
-    long long row = (long long)blockIdx.x * slots + slot;
-    S a, b, g, s;  // r_out, y, dh, dr_out
-    const bool stream = p.dr_out != nullptr;
-    auto fetch = [&]() {
-        const bool ok = row < p.R;
-        const long long at = ok ? row * d : 0;
-        a.load(static_cast<const T *>(p.r) + at, t, tpr, d, ok);
-        g.load(static_cast<const T *>(p.dh) + at, t, tpr, d, ok);
-        s.load(static_cast<const T *>(p.dr_out) + at, t, tpr, d, ok && stream);
-        if constexpr (ADD) b.load(static_cast<const T *>(p.y) + at, t, tpr, d, ok);
-    };
-    fetch();
     const float inv_d = 1.f / d;
-    int parity = 0;
+    int parity = 0, stage = 0;
     for (long long base = (long long)blockIdx.x * slots; base < p.R; base += step, parity ^= 1) {
-        const S ca = a, cg = g, cs = s, cb = b;  // as stored: widened again behind the sums
-        float sum[2] = {0.f, 0.f};
-        {
-            float v[E], e_[E];
-            ca.get(v);
-            cg.get(e_);
+        fetch(Rows::last(stage));
+        rows.wait();
+        float v[E], x[E], sum[2] = {0.f, 0.f};
+        rows.get(stage, 0, v);
+        rows.get(stage, 1, x);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                sum[0] = fmaf(v[e], v[e], sum[0]);
-                sum[1] = fmaf(e_[e] * wt[e], v[e], sum[1]);
-            }
+        for (int e = 0; e < E; ++e) {
+            sum[0] = fmaf(v[e], v[e], sum[0]);
+            sum[1] = fmaf(x[e] * wt[e], v[e], sum[1]);
         }
-        const bool ok = row < p.R;
-        const long long at = row * d;
-        row += step;
-        fetch();
         row_sum<2>(sum, tpr, slot, red, parity);
         const float rstd = inv_rms(sum[0] * inv_d, p.eps);
         const float m = sum[1] * inv_d * rstd * rstd;  // mean(e n) r
-        float v[E], x[E];
-        ca.get(v);
-        cg.get(x);
+        rows.get(stage, 0, v);  // widened again: held across the sums they would take registers
+        rows.get(stage, 1, x);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             dw[e] = fmaf(x[e], v[e] * rstd, dw[e]);
             x[e] = fmaf(-v[e], m, x[e] * wt[e]) * rstd;
         }
-        cs.get(v);
+        rows.get(stage, 2, v);
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] += v[e];
         if constexpr (ADD) {
-            cb.get(v);
+            rows.get(stage, 3, v);
 #pragma unroll
             for (int e = 0; e < E; ++e) ds[e] = fmaf(x[e], v[e], ds[e]);
         }
-        if (ok) {
-            S::store(static_cast<T *>(p.dr) + at, t, tpr, d, x);
+        if (row < p.R) {
+            rows.store(static_cast<T *>(p.dr) + row * d, x);
             if (p.dy) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) x[e] *= sc[e];
-                S::store(static_cast<T *>(p.dy) + at, t, tpr, d, x);
+                rows.store(static_cast<T *>(p.dy) + row * d, x);
             }
         }
+        row += step;
+        stage = Rows::next(stage);
     }
+    Rows::wait_all();
+    float *buf = reinterpret_cast<float *>(smem);
     if (p.dweight) block_part<VEC, NC>(dw, t, tpr, slot, slots, d, p.ws + (long long)blockIdx.x * d, buf);
     if constexpr (ADD)
         if (p.dscale)
@@ -477,13 +560,11 @@ __global__ void __launch_bounds__(32 * kSegments) sum_parts_kernel(const float *
 // ---- launches
 
 // How a row of d channels is laid on threads: 8 channels a thread (16 beyond
-// 8192), so that the accumulators of the weights' gradients stay in registers.
+// 2048), so that the accumulators of the weights' gradients stay in registers.
 struct Layout {
-    int tpr, threads, slots, per_sm;
-    bool wide;  // 16 channels a thread
+    int tpr, threads, slots;
     explicit Layout(int d) {
-        wide = d > 8192;
-        const int need = (d + (wide ? 15 : 7)) / (wide ? 16 : 8);
+        const int each = d > 2048 ? 16 : 8, need = (d + each - 1) / each;
         if (need > 32) {
             tpr = (need + 31) / 32 * 32;
         } else {
@@ -492,42 +573,71 @@ struct Layout {
         }
         slots = tpr >= 256 ? 1 : 256 / tpr;
         threads = tpr * slots;
-        per_sm = threads > 1024 ? 1 : 1024 / threads;
     }
-    // blocks for `rows` rows, at least `least` rows each where there are as many
-    int blocks(long long rows, int least) const {
+    // blocks for `rows` rows: `per_sm` (of at most 256 threads) on every SM, at
+    // least `least` rows each where there are as many
+    int blocks(long long rows, int per_sm, int least) const {
         const long long want = (rows + (long long)slots * least - 1) / ((long long)slots * least);
-        return (int)(want < (long long)kSms * per_sm ? want : (long long)kSms * per_sm);
+        const int held = 256 * per_sm / threads > 1 ? 256 * per_sm / threads : 1;
+        return (int)(want < (long long)kSms * held ? want : (long long)kSms * held);
     }
 };
 
 bool vec_ok(const void *p) { return !p || (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool two_ok(const void *p) { return !p || (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// go(VEC, NC, threads' limit): 16-byte pieces where `vec`, else single elements
-template <typename T, typename F> int with_layout(const Layout &lay, bool vec, F go) {
-    constexpr int V = 16 / sizeof(T), N = 8 / V;
+// the widest pieces that all of the arrays and strides allow: 16 bytes, two
+// bf16, or single elements
+template <typename T> int pieces(std::initializer_list<const void *> arrays, std::initializer_list<long long> strides) {
+    bool wide = true, two = sizeof(T) == 2;
+    for (const void *p : arrays) wide = wide && vec_ok(p), two = two && two_ok(p);
+    for (long long s : strides) wide = wide && s % (16 / (int)sizeof(T)) == 0, two = two && s % 2 == 0;
+    return wide ? 16 / (int)sizeof(T) : two ? 2 : 1;
+}
+
+// go(VEC, NC, threads' limit) for 8 or 16 channels a thread
+template <typename T, typename F> int with_layout(const Layout &lay, int d, int vec, F go) {
     using std::integral_constant;
-    if (lay.wide)
-        return vec ? go(integral_constant<int, V>(), integral_constant<int, 2 * N>(), integral_constant<int, 1024>())
-                   : go(integral_constant<int, 1>(), integral_constant<int, 16>(), integral_constant<int, 1024>());
-    if (lay.threads > 256)
-        return vec ? go(integral_constant<int, V>(), integral_constant<int, N>(), integral_constant<int, 1024>())
-                   : go(integral_constant<int, 1>(), integral_constant<int, 8>(), integral_constant<int, 1024>());
-    return vec ? go(integral_constant<int, V>(), integral_constant<int, N>(), integral_constant<int, 256>())
-               : go(integral_constant<int, 1>(), integral_constant<int, 8>(), integral_constant<int, 256>());
+    auto sized = [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        if (lay.threads > 512)
+            return go(v, integral_constant<int, 16 / V>(), integral_constant<int, 1024>());
+        if (d > 2048)
+            return go(v, integral_constant<int, 16 / V>(), integral_constant<int, 512>());
+        return go(v, integral_constant<int, 8 / V>(), integral_constant<int, 256>());
+    };
+    if (vec == 16 / (int)sizeof(T)) return sized(integral_constant<int, 16 / (int)sizeof(T)>());
+    if constexpr (sizeof(T) == 2)
+        if (vec == 2) return sized(integral_constant<int, 2>());
+    return sized(integral_constant<int, 1>());
 }
 
-template <typename T> bool gate_vec(const NormGateParams &p) {
-    const int v = 16 / sizeof(T);
-    return p.d % v == 0 && p.o_sb % v == 0 && p.o_sh % v == 0 && p.o_sl % v == 0 && vec_ok(p.o) &&
-           vec_ok(p.gate) && (!p.gate || p.ldg % v == 0);
+// shared memory of a block of `threads`: the rows ahead; the block's sums use it later
+template <typename T, int VEC, int NC, int A, int MT> constexpr size_t ring_bytes(int threads) {
+    const size_t ring = (size_t)threads * Ahead<T, VEC, NC, A, MT>::kBytes, sums = (size_t)threads * VEC * NC * sizeof(float);
+    return ring > sums ? ring : sums;
 }
 
-int gate_parts(const Layout &lay, const NormGateParams &p, int least) {
+// a launch with its dynamic shared memory; `most`, what the kernel's largest
+// block takes, is allowed once per kernel and device
+template <auto kernel, typename... A>
+int launch(unsigned grid, int threads, size_t smem, size_t most, cudaStream_t s, const A &...args) {
+    static std::atomic<unsigned> allowed{0};
+    int dev = 0;
+    if (most > 32 * 1024 && cudaGetDevice(&dev) == cudaSuccess && (dev >= 32 || !(allowed.load() >> dev & 1))) {
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        if (dev < 32) allowed.fetch_or(1u << dev);
+    }
+    kernel<<<grid, threads, smem, s>>>(args...);
+    return 0;
+}
+
+int gate_parts(const Layout &lay, const NormGateParams &p, int per_sm, int least) {
     const long long rows = (long long)p.B * p.L * (p.per_head ? 1 : p.H);
-    if (!p.per_head) return lay.blocks(rows, least);
+    const int all = lay.blocks(rows, per_sm, least);
+    if (!p.per_head) return all;
     // every head has blocks of its own: share the device's between them
-    const int all = lay.blocks(rows, least), share = (kSms * lay.per_sm + p.H - 1) / p.H;
+    const int share = (lay.blocks(1ll << 60, per_sm, 1) + p.H - 1) / p.H;
     return all < share ? all : share;
 }
 
@@ -539,43 +649,37 @@ size_t norm_gate_bwd_ws_bytes(int, int B, int H, int L, int d) {
     p.B = B; p.H = H; p.L = L;
     size_t most = 0;
     for (p.per_head = 0; p.per_head < 2; ++p.per_head) {
-        const size_t n = (size_t)gate_parts(lay, p, kMinRows) * (p.per_head ? H : 1) * d;
+        const size_t n = (size_t)gate_parts(lay, p, bwd_blocks(256), kMinRows) * (p.per_head ? H : 1) * d;
         most = n > most ? n : most;
     }
     return sizeof(float) * most;
 }
 size_t residual_norm_bwd_ws_bytes(int, int R, int D) {
-    return sizeof(float) * 2 * (size_t)Layout(D).blocks(R, kMinRows) * D;
+    return sizeof(float) * 2 * (size_t)Layout(D).blocks(R, bwd_blocks(256), kMinRows) * D;
 }
 
 template <typename T> int launch_norm_gate(const NormGateParams &p, cudaStream_t s) {
     const Layout lay(p.d);
-    const bool vec = gate_vec<T>(p) && vec_ok(p.out);
-    const int parts = gate_parts(lay, p, 1);
+    const int vec = pieces<T>({p.o, p.gate, p.out}, {p.d, p.o_sb, p.o_sh, p.o_sl, p.gate ? p.ldg : 0});
+    const int parts = gate_parts(lay, p, fwd_blocks(256), 1);
     const unsigned grid = (unsigned)parts * (p.per_head ? p.H : 1);
-    return with_layout<T>(lay, vec, [&](auto v, auto nc, auto mt) {
-        if (p.gate)
-            norm_gate_kernel<T, v(), nc(), mt(), true><<<grid, lay.threads, 0, s>>>(p, lay.tpr, parts);
-        else
-            norm_gate_kernel<T, v(), nc(), mt(), false><<<grid, lay.threads, 0, s>>>(p, lay.tpr, parts);
-        return 0;
+    return with_layout<T>(lay, p.d, vec, [&](auto v, auto nc, auto mt) {
+        constexpr int V = v(), N = nc(), M = mt();
+        return p.gate ? launch<norm_gate_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 2, M>(lay.threads), ring_bytes<T, V, N, 2, M>(M), s, p, lay.tpr, parts)
+                      : launch<norm_gate_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 1, M>(lay.threads), ring_bytes<T, V, N, 1, M>(M), s, p, lay.tpr, parts);
     });
 }
 
 template <typename T> int launch_norm_gate_bwd(const NormGateParams &p, cudaStream_t s) {
     const Layout lay(p.d);
-    const int v16 = 16 / sizeof(T);
-    const bool vec = gate_vec<T>(p) && vec_ok(p.dout) && vec_ok(p.d_o) &&
-                     vec_ok(p.dgate) && p.do_sb % v16 == 0 && p.do_sh % v16 == 0 && p.do_sl % v16 == 0 &&
-                     (!p.dgate || p.lddg % v16 == 0);
-    const int parts = gate_parts(lay, p, kMinRows);
+    const int vec = pieces<T>({p.o, p.gate, p.dout, p.d_o, p.dgate},
+                              {p.d, p.o_sb, p.o_sh, p.o_sl, p.do_sb, p.do_sh, p.do_sl, p.gate ? p.ldg : 0, p.gate ? p.lddg : 0});
+    const int parts = gate_parts(lay, p, bwd_blocks(256), kMinRows);
     const unsigned grid = (unsigned)parts * (p.per_head ? p.H : 1);
-    with_layout<T>(lay, vec, [&](auto v, auto nc, auto mt) {
-        if (p.gate)
-            norm_gate_bwd_kernel<T, v(), nc(), mt(), true><<<grid, lay.threads, 0, s>>>(p, lay.tpr, parts);
-        else
-            norm_gate_bwd_kernel<T, v(), nc(), mt(), false><<<grid, lay.threads, 0, s>>>(p, lay.tpr, parts);
-        return 0;
+    with_layout<T>(lay, p.d, vec, [&](auto v, auto nc, auto mt) {
+        constexpr int V = v(), N = nc(), M = mt();
+        return p.gate ? launch<norm_gate_bwd_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 3, M>(lay.threads), ring_bytes<T, V, N, 3, M>(M), s, p, lay.tpr, parts)
+                      : launch<norm_gate_bwd_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 2, M>(lay.threads), ring_bytes<T, V, N, 2, M>(M), s, p, lay.tpr, parts);
     });
     if (!p.dweight) return 0;
     const long long n = (long long)p.d * (p.per_head ? p.H : 1);
@@ -585,30 +689,23 @@ template <typename T> int launch_norm_gate_bwd(const NormGateParams &p, cudaStre
 
 template <typename T> int launch_residual_norm(const ResidualNormParams &p, cudaStream_t s) {
     const Layout lay(p.D);
-    const bool vec = p.D % (16 / (int)sizeof(T)) == 0 && vec_ok(p.r) && vec_ok(p.y) &&
-                     vec_ok(p.r_out) && vec_ok(p.h);
-    const unsigned grid = (unsigned)lay.blocks(p.R, 1);
-    return with_layout<T>(lay, vec, [&](auto v, auto nc, auto mt) {
-        if (p.y)
-            residual_norm_kernel<T, v(), nc(), mt(), true><<<grid, lay.threads, 0, s>>>(p, lay.tpr);
-        else
-            residual_norm_kernel<T, v(), nc(), mt(), false><<<grid, lay.threads, 0, s>>>(p, lay.tpr);
-        return 0;
+    const int vec = pieces<T>({p.r, p.y, p.r_out, p.h}, {p.D});
+    const unsigned grid = (unsigned)lay.blocks(p.R, fwd_blocks(256), 1);
+    return with_layout<T>(lay, p.D, vec, [&](auto v, auto nc, auto mt) {
+        constexpr int V = v(), N = nc(), M = mt();
+        return p.y ? launch<residual_norm_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 2, M>(lay.threads), ring_bytes<T, V, N, 2, M>(M), s, p, lay.tpr)
+                   : launch<residual_norm_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 1, M>(lay.threads), ring_bytes<T, V, N, 1, M>(M), s, p, lay.tpr);
     });
 }
 
 template <typename T> int launch_residual_norm_bwd(const ResidualNormParams &p, cudaStream_t s) {
     const Layout lay(p.D);
-    const bool vec = p.D % (16 / (int)sizeof(T)) == 0 && vec_ok(p.r) && vec_ok(p.y) &&
-                     vec_ok(p.dh) && vec_ok(p.dr_out) && vec_ok(p.dr) &&
-                     vec_ok(p.dy);
-    const unsigned grid = (unsigned)lay.blocks(p.R, kMinRows);
-    with_layout<T>(lay, vec, [&](auto v, auto nc, auto mt) {
-        if (p.y)
-            residual_norm_bwd_kernel<T, v(), nc(), mt(), true><<<grid, lay.threads, 0, s>>>(p, lay.tpr);
-        else
-            residual_norm_bwd_kernel<T, v(), nc(), mt(), false><<<grid, lay.threads, 0, s>>>(p, lay.tpr);
-        return 0;
+    const int vec = pieces<T>({p.r, p.y, p.dh, p.dr_out, p.dr, p.dy}, {p.D});
+    const unsigned grid = (unsigned)lay.blocks(p.R, bwd_blocks(256), kMinRows);
+    with_layout<T>(lay, p.D, vec, [&](auto v, auto nc, auto mt) {
+        constexpr int V = v(), N = nc(), M = mt();
+        return p.y ? launch<residual_norm_bwd_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 4, M>(lay.threads), ring_bytes<T, V, N, 4, M>(M), s, p, lay.tpr)
+                   : launch<residual_norm_bwd_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 3, M>(lay.threads), ring_bytes<T, V, N, 3, M>(M), s, p, lay.tpr);
     });
     if (p.dweight || p.dscale)
         sum_parts_kernel<<<dim3((unsigned)((p.D + 31) / 32), p.dscale ? 2 : 1), 32 * kSegments, 0, s>>>(

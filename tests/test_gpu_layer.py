@@ -250,6 +250,7 @@ GATE = [
     (2, 12, 100, 64, "shared", True), (1, 1, 70, 2048, "shared", True), (1, 2, 9, 300, "head", True), (2, 1, 4, 16384, "none", True),
     (1, 5, 40, 33, "head", False), (2, 2, 17, 256, "none", False), (1, 1, 3, 5001, "shared", True), (3, 7, 121, 48, "head", True),
     (1, 40, 300, 32, "shared", True), (1, 3, 1, 511, "shared", True), (1, 1, 200, 260, "head", True), (2, 130, 2, 8, "head", True),
+    (1, 2, 3, 2056, "head", True), (1, 1, 9, 8190, "shared", True), (2, 1, 5, 6000, "none", False), (1, 4, 1200, 2, "head", True),
 ]
 
 
@@ -342,6 +343,7 @@ RESIDUAL = [
     (130, 768, True, True, True, True), (7, 1111, True, True, True, False), (2, 16384, True, True, True, True), (9, 4096, False, False, True, True),
     (1, 5003, True, True, False, True), (300, 64, True, True, True, True), (4, 8192, True, False, False, True), (1000, 24, True, True, True, True),
     (33, 260, False, False, True, False), (2, 9001, True, True, True, True),
+    (3, 2056, True, True, True, True), (5, 7096, True, True, True, True), (4, 6002, True, True, True, True),
 ]
 
 
