@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kSms = 148;
 constexpr int kMinRows = 4;     // rows that a block walks at least, where weights' gradients are wanted
-constexpr int kSegments = 8;    // partial sums joined side by side
+constexpr int kSegments = 32;   // partial sums joined side by side
 constexpr int kMaxRows = 3;     // rows of a thread in shared memory: the present one and two on their way
 
 // 1/sqrt(ms + eps); a row of zeros with eps = 0 is left as zeros
@@ -90,18 +90,21 @@ __device__ __forceinline__ void narrow(Piece<float, 1> &p, const float *f) { p.v
 
 // ---- a thread's pieces of the present row and of those to come, A arrays each:
 // S rows in shared memory (three where they fit the block's, whatever fits
-// otherwise), S - 1 of them on their way.  Two-byte pieces have no
-// asynchronous copy and the widest fp32 rows no room: S = 0, read when used.
+// otherwise), S - 1 of them on their way.  Two-byte pieces have no asynchronous
+// copy: the next row's are loaded into registers.  The widest fp32 rows have no
+// room at all (S = 0) and are read when used.
 template <typename T, int VEC, int NC, int A, int MT> struct Ahead {
     using P = Piece<T, VEC>;
     static constexpr int kRow = A * NC * (int)sizeof(P);  // bytes per thread
     static constexpr int kFit = 200 * 1024 / (MT * kRow);
-    static constexpr int S = sizeof(P) == 2 ? 0 : kFit < kMaxRows ? kFit : kMaxRows;
-    static constexpr int kAhead = S > 0 ? S - 1 : 0;
+    static constexpr bool kHeld = sizeof(P) == 2;
+    static constexpr int S = kHeld ? 0 : kFit < kMaxRows ? kFit : kMaxRows;
+    static constexpr int kAhead = S > 0 ? S - 1 : kHeld ? 1 : 0;
     static constexpr int kBytes = S * kRow;
     P *mine;
     int t, tpr, d, threads;
-    const T *at[S == 0 ? A : 1];  // S = 0: the present row
+    const T *at[S == 0 && !kHeld ? A : 1];    // S = 0: the present row
+    P held[kHeld ? A : 1][NC], next_[kHeld ? A : 1][NC];
 
     __device__ __forceinline__ Ahead(uint8_t *smem, int t_, int tpr_, int d_)
         : mine(reinterpret_cast<P *>(smem) + threadIdx.x), t(t_), tpr(tpr_), d(d_), threads(blockDim.x) {}
@@ -110,7 +113,15 @@ template <typename T, int VEC, int NC, int A, int MT> struct Ahead {
     }
     // array a of a row (zeros where not ok, and behind the row's end)
     __device__ __forceinline__ void fetch(int stage, int a, const T *row, bool ok) {
-        if constexpr (S == 0) {
+        if constexpr (kHeld) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                const int c = (j * tpr + t) * VEC;
+                held[a][j] = next_[a][j];
+                next_[a][j].v = 0;
+                if (ok && c < d) next_[a][j] = *reinterpret_cast<const P *>(row + c);
+            }
+        } else if constexpr (S == 0) {
             at[a] = ok ? row : nullptr;
         } else {
 #pragma unroll
@@ -140,7 +151,9 @@ template <typename T, int VEC, int NC, int A, int MT> struct Ahead {
     __device__ __forceinline__ void get(int stage, int a, float *f) const {
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            if constexpr (S == 0) {
+            if constexpr (kHeld) {
+                widen(held[a][j], f + j * VEC);
+            } else if constexpr (S == 0) {
                 const int c = (j * tpr + t) * VEC;
                 P v{};
                 if (at[a] && c < d) v = *reinterpret_cast<const P *>(at[a] + c);
@@ -233,87 +246,84 @@ __device__ __forceinline__ void block_part(float *acc, int t, int tpr, int slot,
 }
 
 // ---- the rows of the gated norm: (b, l, h) with h innermost, or, where a
-// block stays with one head, (b, l)
-struct GateRows {
-    long long o, g, out, d_o, dg;  // offsets of the row's first channel
-    int b, l, h;                   // h counts inside `heads`
-};
-
-__device__ __forceinline__ void gate_offsets(const NormGateParams &p, GateRows &r, int h) {
-    const long long token = (long long)r.b * p.L + r.l;
-    r.o = r.b * p.o_sb + h * p.o_sh + r.l * p.o_sl;
-    r.d_o = r.b * p.do_sb + h * p.do_sh + r.l * p.do_sl;
-    r.out = (token * p.H + h) * p.d;
-    r.g = token * p.ldg + (long long)h * p.d;
-    r.dg = token * p.lddg + (long long)h * p.d;
+// block stays with one head, (b, l).  Positions are found anew for every row,
+// by two multiplications for divisions: a walk that steps offsets along keeps
+// twenty registers more, which the backward pass has not (38 against 30 us).
+FastDiv fast_div(unsigned by) {
+    // n / by = n * ceil(2^(31 + s) / by) >> (31 + s), s = ceil(log2 by), for n < 2^31
+    FastDiv f{by, 0, 0};
+    while ((1u << f.shift) < by) ++f.shift;
+    f.factor = (unsigned)(((1ull << (31 + f.shift)) + by - 1) / by);
+    return f;
+}
+__device__ __forceinline__ unsigned divide(unsigned n, const FastDiv &f) {
+    return f.by == 1 ? n : __umulhi(n, f.factor) >> (f.shift - 1);
 }
 
-struct GateWalk {
-    int heads, h0;                 // heads that the rows run over, from h0
-    long long rows, row, step;
-    int db, dl, dh;                // the step in rows, taken apart
-    __device__ __forceinline__ void begin(const NormGateParams &p, int parts, int slots, int slot, GateRows &r) {
-        heads = p.per_head ? 1 : p.H;
-        h0 = p.per_head ? blockIdx.x / parts : 0;
-        rows = (long long)p.B * p.L * heads;
-        row = (long long)(blockIdx.x % parts) * slots + slot;
-        step = (long long)parts * slots;
-        dh = (int)(step % heads);
-        const long long dt = step / heads;
-        dl = (int)(dt % p.L);
-        db = (int)(dt / p.L);
-        r.h = (int)(row % heads);
-        const long long token = row / heads;
-        r.l = (int)(token % p.L);
-        r.b = (int)(token / p.L);
+struct GatePlace {
+    long long token;
+    int b, l, h;
+    // row `row` of the kernel's; `head`: the block's, or 0
+    __device__ __forceinline__ GatePlace(const NormGateParams &p, long long row, int head) {
+        if (p.small) {
+            const unsigned n = (unsigned)row, t = divide(n, p.heads);
+            token = t;
+            h = head + (int)(n - t * p.heads.by);
+            b = (int)divide(t, p.tokens);
+            l = (int)(t - (unsigned)b * p.tokens.by);
+        } else {
+            token = row / p.heads.by;
+            h = head + (int)(row - token * p.heads.by);
+            b = (int)(token / p.L);
+            l = (int)(token - (long long)b * p.L);
+        }
     }
-    __device__ __forceinline__ void next(const NormGateParams &p, GateRows &r) {
-        row += step;
-        r.h += dh;
-        r.l += dl;
-        r.b += db;
-        if (r.h >= heads) { r.h -= heads; ++r.l; }
-        if (r.l >= p.L) { r.l -= p.L; ++r.b; }
+    __device__ __forceinline__ long long strided(long long sb, long long sh, long long sl) const {
+        return b * sb + h * sh + l * sl;
+    }
+    __device__ __forceinline__ long long packed(const NormGateParams &p, long long ld) const {
+        return token * ld + (long long)h * p.d;
     }
 };
+
+// the offset of a row in an array of tokens without gaps (out, dout)
+__device__ __forceinline__ long long packed_row(const NormGateParams &p, long long row, int head) {
+    return (p.per_head ? row * p.H + head : row) * p.d;
+}
 
 // Blocks per SM that the registers have to leave room for: threads up to 256,
 // 512 (16 channels each) and 1024 (rows beyond 8192).
-constexpr int fwd_blocks(int mt) { return mt == 256 ? 4 : 1; }
-constexpr int bwd_blocks(int mt) { return mt == 256 ? 3 : 1; }
+constexpr int fwd_blocks(int mt, int each = 8) { return mt > 256 ? 1 : each == 8 ? 4 : each == 16 ? 3 : 2; }
+constexpr int bwd_blocks(int mt, int vec = 8, int each = 8) { return mt > 256 ? 1 : vec == 1 || each == 16 ? 2 : 3; }
 
 template <typename T, int VEC, int NC, int MT, bool GATE>
-__global__ void __launch_bounds__(MT, fwd_blocks(MT)) norm_gate_kernel(NormGateParams p, int tpr, int parts) {
+__global__ void __launch_bounds__(MT, fwd_blocks(MT, VEC * NC)) norm_gate_kernel(NormGateParams p, int tpr, int parts) {
     constexpr int E = VEC * NC;
     using Rows = Ahead<T, VEC, NC, GATE ? 2 : 1, MT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][32][2];
     const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, d = p.d;
     Rows rows(smem, t, tpr, d);
-    GateRows r, next;
-    GateWalk w, ahead;
-    w.begin(p, parts, slots, slot, r);
-    ahead = w;
-    next = r;
+    const int head = p.per_head ? blockIdx.x / parts : 0;
+    const long long first = (long long)(blockIdx.x % parts) * slots, step = (long long)parts * slots;
+    const long long end = (long long)p.B * p.L * (p.per_head ? 1 : p.H);
+    long long ahead = first + slot;
     auto fetch = [&](int stage) {
-        const bool ok = ahead.row < ahead.rows;
-        if (ok) gate_offsets(p, next, ahead.h0 + next.h);
-        else next.o = next.g = 0;
-        rows.fetch(stage, 0, static_cast<const T *>(p.o) + next.o, ok);
-        if constexpr (GATE) rows.fetch(stage, 1, static_cast<const T *>(p.gate) + next.g, ok);
+        const bool ok = ahead < end;
+        const GatePlace at(p, ok ? ahead : 0, head);
+        rows.fetch(stage, 0, static_cast<const T *>(p.o) + at.strided(p.o_sb, p.o_sh, p.o_sl), ok);
+        if constexpr (GATE) rows.fetch(stage, 1, static_cast<const T *>(p.gate) + at.packed(p, p.ldg), ok);
         rows.close();
-        ahead.next(p, next);
+        ahead += step;
     };
     for (int i = 0; i < Rows::kAhead; ++i) fetch(i);
     float wt[E];
-    load_weights<VEC, NC>(wt, p.weight ? p.weight + (long long)w.h0 * d : nullptr, t, tpr, d);
-    const long long first = (long long)(blockIdx.x % parts) * slots;
+    load_weights<VEC, NC>(wt, p.weight ? p.weight + (long long)head * d : nullptr, t, tpr, d);
     int parity = 0, stage = 0;
-    for (long long base = first; base < w.rows; base += w.step, parity ^= 1) {
+    for (long long base = first; base < end; base += step, parity ^= 1) {
         fetch(Rows::last(stage));
         rows.wait();
         float ov[E], sum[1] = {0.f};
-        const bool ok = w.row < w.rows;
         rows.get(stage, 0, ov);
 #pragma unroll
         for (int e = 0; e < E; ++e) sum[0] = fmaf(ov[e], ov[e], sum[0]);
@@ -327,51 +337,44 @@ __global__ void __launch_bounds__(MT, fwd_blocks(MT)) norm_gate_kernel(NormGateP
 #pragma unroll
             for (int e = 0; e < E; ++e) ov[e] *= zv[e] * sigmoid(zv[e]);
         }
-        if (ok) {
-            gate_offsets(p, r, w.h0 + r.h);
-            rows.store(static_cast<T *>(p.out) + r.out, ov);
-        }
-        w.next(p, r);
+        const long long row = base + slot;
+        if (row < end) rows.store(static_cast<T *>(p.out) + packed_row(p, row, head), ov);
         stage = Rows::next(stage);
     }
 }
 
 template <typename T, int VEC, int NC, int MT, bool GATE>
-__global__ void __launch_bounds__(MT, bwd_blocks(MT)) norm_gate_bwd_kernel(NormGateParams p, int tpr, int parts) {
+__global__ void __launch_bounds__(MT, bwd_blocks(MT, VEC, VEC * NC)) norm_gate_bwd_kernel(NormGateParams p, int tpr, int parts) {
     constexpr int E = VEC * NC;
     using Rows = Ahead<T, VEC, NC, GATE ? 3 : 2, MT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][32][2];
     const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, d = p.d;
     Rows rows(smem, t, tpr, d);
-    GateRows r, next;
-    GateWalk w, ahead;
-    w.begin(p, parts, slots, slot, r);
-    ahead = w;
-    next = r;
+    const int head = p.per_head ? blockIdx.x / parts : 0;
+    const long long first = (long long)(blockIdx.x % parts) * slots, step = (long long)parts * slots;
+    const long long end = (long long)p.B * p.L * (p.per_head ? 1 : p.H);
+    long long ahead = first + slot;
     auto fetch = [&](int stage) {
-        const bool ok = ahead.row < ahead.rows;
-        if (ok) gate_offsets(p, next, ahead.h0 + next.h);
-        else next.o = next.out = next.g = 0;
-        rows.fetch(stage, 0, static_cast<const T *>(p.o) + next.o, ok);
-        rows.fetch(stage, 1, static_cast<const T *>(p.dout) + next.out, ok);
-        if constexpr (GATE) rows.fetch(stage, 2, static_cast<const T *>(p.gate) + next.g, ok);
+        const bool ok = ahead < end;
+        const GatePlace at(p, ok ? ahead : 0, head);
+        rows.fetch(stage, 0, static_cast<const T *>(p.o) + at.strided(p.o_sb, p.o_sh, p.o_sl), ok);
+        rows.fetch(stage, 1, static_cast<const T *>(p.dout) + packed_row(p, ok ? ahead : 0, head), ok);
+        if constexpr (GATE) rows.fetch(stage, 2, static_cast<const T *>(p.gate) + at.packed(p, p.ldg), ok);
         rows.close();
-        ahead.next(p, next);
+        ahead += step;
     };
     for (int i = 0; i < Rows::kAhead; ++i) fetch(i);
     float wt[E], dw[E];
-    load_weights<VEC, NC>(wt, p.weight ? p.weight + (long long)w.h0 * d : nullptr, t, tpr, d);
+    load_weights<VEC, NC>(wt, p.weight ? p.weight + (long long)head * d : nullptr, t, tpr, d);
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[e] = 0.f;
-    const long long first = (long long)(blockIdx.x % parts) * slots;
     const float inv_d = 1.f / d;
     int parity = 0, stage = 0;
-    for (long long base = first; base < w.rows; base += w.step, parity ^= 1) {
+    for (long long base = first; base < end; base += step, parity ^= 1) {
         fetch(Rows::last(stage));
         rows.wait();
         float ov[E], zv[E], gv[E], sum[2] = {0.f, 0.f};
-        const bool ok = w.row < w.rows;
         rows.get(stage, 0, ov);
         rows.get(stage, 1, gv);
         if constexpr (GATE) rows.get(stage, 2, zv);
@@ -395,23 +398,24 @@ __global__ void __launch_bounds__(MT, bwd_blocks(MT)) norm_gate_bwd_kernel(NormG
             ov[e] = fmaf(-ov[e], m, gv[e] * wt[e]) * rstd;
             if constexpr (GATE) zv[e] *= rstd;
         }
-        if (ok) {
-            gate_offsets(p, r, w.h0 + r.h);
-            rows.store(static_cast<T *>(p.d_o) + r.d_o, ov);
-            if constexpr (GATE) rows.store(static_cast<T *>(p.dgate) + r.dg, zv);
+        const long long row = base + slot;
+        if (row < end) {
+            const GatePlace at(p, row, head);
+            rows.store(static_cast<T *>(p.d_o) + at.strided(p.do_sb, p.do_sh, p.do_sl), ov);
+            if constexpr (GATE) rows.store(static_cast<T *>(p.dgate) + at.packed(p, p.lddg), zv);
         }
-        w.next(p, r);
         stage = Rows::next(stage);
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Rows::wait_all();  // the block's sums take the copies' place
     if (p.dweight)
         block_part<VEC, NC>(dw, t, tpr, slot, slots, d,
-                            p.ws + ((long long)(blockIdx.x % parts) * (p.per_head ? p.H : 1) + w.h0) * d,
+                            p.ws + ((long long)(blockIdx.x % parts) * (p.per_head ? p.H : 1) + head) * d,
                             reinterpret_cast<float *>(smem));
 }
 
 template <typename T, int VEC, int NC, int MT, bool ADD>
-__global__ void __launch_bounds__(MT, fwd_blocks(MT)) residual_norm_kernel(ResidualNormParams p, int tpr) {
+__global__ void __launch_bounds__(MT, fwd_blocks(MT, VEC * NC)) residual_norm_kernel(ResidualNormParams p, int tpr) {
     constexpr int E = VEC * NC;
     using Rows = Ahead<T, VEC, NC, ADD ? 2 : 1, MT>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -459,7 +463,7 @@ __global__ void __launch_bounds__(MT, fwd_blocks(MT)) residual_norm_kernel(Resid
 }
 
 template <typename T, int VEC, int NC, int MT, bool ADD>
-__global__ void __launch_bounds__(MT, bwd_blocks(MT)) residual_norm_bwd_kernel(ResidualNormParams p, int tpr) {
+__global__ void __launch_bounds__(MT, bwd_blocks(MT, VEC, VEC * NC)) residual_norm_bwd_kernel(ResidualNormParams p, int tpr) {
     constexpr int E = VEC * NC;
     using Rows = Ahead<T, VEC, NC, ADD ? 4 : 3, MT>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -527,6 +531,7 @@ __global__ void __launch_bounds__(MT, bwd_blocks(MT)) residual_norm_bwd_kernel(R
         row += step;
         stage = Rows::next(stage);
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Rows::wait_all();
     float *buf = reinterpret_cast<float *>(smem);
     if (p.dweight) block_part<VEC, NC>(dw, t, tpr, slot, slots, d, p.ws + (long long)blockIdx.x * d, buf);
@@ -537,34 +542,43 @@ __global__ void __launch_bounds__(MT, bwd_blocks(MT)) residual_norm_bwd_kernel(R
 
 // out[c] = sum over i of part[i*n + c]: 32 channels per block, kSegments runs
 // of partial sums side by side, joined in order; blockIdx.y takes the second
-// set of partial sums (behind the first) and its output
+// set of partial sums (behind the first) and its output.  Latency is all there
+// is to it: 8 segments took 12 us for 444 partial sums, 32 take 4.  Launched
+// early (programmatic serialisation), it waits here for the sums.
 __global__ void __launch_bounds__(32 * kSegments) sum_parts_kernel(const float *part, int parts, long long n,
                                                                    float *out0, float *out1) {
-    __shared__ float seg[kSegments][32];
+    __shared__ float seg[kSegments][33];
     float *out = blockIdx.y ? out1 : out0;
-    const long long c = (long long)blockIdx.x * 32 + threadIdx.x % 32;
-    const int s = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, s = threadIdx.x / 32;
+    const long long c = (long long)blockIdx.x * 32 + lane;
     const float *at = part + (long long)blockIdx.y * parts * n;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float acc = 0.f;
     if (out && c < n)
-#pragma unroll 8
+#pragma unroll 16
         for (int i = s; i < parts; i += kSegments) acc += at[i * n + c];
-    seg[s][threadIdx.x % 32] = acc;
+    seg[s][lane] = acc;
     __syncthreads();
-    if (s != 0 || !out || c >= n) return;
-#pragma unroll
-    for (int i = 1; i < kSegments; ++i) acc += seg[i][threadIdx.x];
-    out[c] = acc;
+    // warp s joins the segments of channel s
+    static_assert(kSegments == 32, "a warp per channel");
+    float v = group_sum<32>(seg[lane][s]);
+    const long long mine = (long long)blockIdx.x * 32 + s;
+    if (lane == 0 && out && mine < n) out[mine] = v;
 }
 
 // ---- launches
 
-// How a row of d channels is laid on threads: 8 channels a thread (16 beyond
-// 2048), so that the accumulators of the weights' gradients stay in registers.
+// How a row of d channels is laid on threads.  Backward: 8 channels a thread
+// (16 beyond 2048), so that the accumulators of the weights' gradients stay in
+// registers.  Forward there are none, and up to 1024 channels a row stays
+// inside a warp, which needs no barrier: up to 32 a thread (not in single
+// elements, whose loads are held in registers one by one).
 struct Layout {
-    int tpr, threads, slots;
-    explicit Layout(int d) {
-        const int each = d > 2048 ? 16 : 8, need = (d + each - 1) / each;
+    int each, tpr, threads, slots;
+    Layout(int d, bool forward, int vec = 1) {
+        each = d > 2048 ? 16 : 8;
+        if (forward && vec > 1 && d > 256 && d <= 1024) each = (d + 255) / 256 * 8;
+        const int need = (d + each - 1) / each;
         if (need > 32) {
             tpr = (need + 31) / 32 * 32;
         } else {
@@ -581,6 +595,8 @@ struct Layout {
         const int held = 256 * per_sm / threads > 1 ? 256 * per_sm / threads : 1;
         return (int)(want < (long long)kSms * held ? want : (long long)kSms * held);
     }
+    int forward_blocks(long long rows) const { return blocks(rows, fwd_blocks(256, each), 1); }
+    int backward_blocks(long long rows) const { return blocks(rows, bwd_blocks(256, 8, each), kMinRows); }
 };
 
 bool vec_ok(const void *p) { return !p || (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -595,15 +611,18 @@ template <typename T> int pieces(std::initializer_list<const void *> arrays, std
     return wide ? 16 / (int)sizeof(T) : two ? 2 : 1;
 }
 
-// go(VEC, NC, threads' limit) for 8 or 16 channels a thread
-template <typename T, typename F> int with_layout(const Layout &lay, int d, int vec, F go) {
+// go(VEC, NC, threads' limit) for the layout's channels a thread
+template <typename T, bool FORWARD, typename F> int with_layout(const Layout &lay, int vec, F go) {
     using std::integral_constant;
     auto sized = [&](auto v) {
         constexpr int V = decltype(v)::value;
-        if (lay.threads > 512)
-            return go(v, integral_constant<int, 16 / V>(), integral_constant<int, 1024>());
-        if (d > 2048)
-            return go(v, integral_constant<int, 16 / V>(), integral_constant<int, 512>());
+        if (lay.threads > 512) return go(v, integral_constant<int, 16 / V>(), integral_constant<int, 1024>());
+        if (lay.threads > 256) return go(v, integral_constant<int, 16 / V>(), integral_constant<int, 512>());
+        if constexpr (FORWARD && V > 1) {
+            if (lay.each == 24) return go(v, integral_constant<int, 24 / V>(), integral_constant<int, 256>());
+            if (lay.each == 32) return go(v, integral_constant<int, 32 / V>(), integral_constant<int, 256>());
+        }
+        if (lay.each == 16) return go(v, integral_constant<int, 16 / V>(), integral_constant<int, 256>());
         return go(v, integral_constant<int, 8 / V>(), integral_constant<int, 256>());
     };
     if (vec == 16 / (int)sizeof(T)) return sized(integral_constant<int, 16 / (int)sizeof(T)>());
@@ -632,66 +651,91 @@ int launch(unsigned grid, int threads, size_t smem, size_t most, cudaStream_t s,
     return 0;
 }
 
-int gate_parts(const Layout &lay, const NormGateParams &p, int per_sm, int least) {
-    const long long rows = (long long)p.B * p.L * (p.per_head ? 1 : p.H);
-    const int all = lay.blocks(rows, per_sm, least);
-    if (!p.per_head) return all;
+// sum_parts_kernel behind the kernel that writes the sums, its launch overlapping that one's end
+int launch_sums(const float *part, int parts, long long n, float *out0, float *out1, cudaStream_t s) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)((n + 31) / 32), out1 ? 2 : 1);
+    c.blockDim = dim3(32 * kSegments);
+    c.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    if (cudaLaunchKernelEx(&c, sum_parts_kernel, part, parts, n, out0, out1) == cudaSuccess) return 0;
+    cudaGetLastError();
+    return -7;
+}
+
+// the blocks of the gated norm, per head where each stays with one
+int gate_parts(const Layout &lay, const NormGateParams &p, bool forward) {
+    auto blocks = [&](long long rows) { return forward ? lay.forward_blocks(rows) : lay.backward_blocks(rows); };
+    if (!p.per_head) return blocks((long long)p.B * p.L * p.H);
     // every head has blocks of its own: share the device's between them
-    const int share = (lay.blocks(1ll << 60, per_sm, 1) + p.H - 1) / p.H;
+    const int all = blocks((long long)p.B * p.L), share = (blocks(1ll << 60) + p.H - 1) / p.H;
     return all < share ? all : share;
+}
+
+// p with its divisions
+NormGateParams divided(NormGateParams p) {
+    p.heads = fast_div(p.per_head ? 1u : (unsigned)p.H);
+    p.tokens = fast_div((unsigned)p.L);
+    p.small = (long long)p.B * p.L * p.heads.by < (1ll << 31);
+    return p;
 }
 
 }  // namespace
 
 size_t norm_gate_bwd_ws_bytes(int, int B, int H, int L, int d) {
-    const Layout lay(d);
+    const Layout lay(d, false);
     NormGateParams p{};
     p.B = B; p.H = H; p.L = L;
     size_t most = 0;
     for (p.per_head = 0; p.per_head < 2; ++p.per_head) {
-        const size_t n = (size_t)gate_parts(lay, p, bwd_blocks(256), kMinRows) * (p.per_head ? H : 1) * d;
+        const size_t n = (size_t)gate_parts(lay, p, false) * (p.per_head ? H : 1) * d;
         most = n > most ? n : most;
     }
     return sizeof(float) * most;
 }
 size_t residual_norm_bwd_ws_bytes(int, int R, int D) {
-    return sizeof(float) * 2 * (size_t)Layout(D).blocks(R, bwd_blocks(256), kMinRows) * D;
+    return sizeof(float) * 2 * (size_t)Layout(D, false).backward_blocks(R) * D;
 }
 
-template <typename T> int launch_norm_gate(const NormGateParams &p, cudaStream_t s) {
-    const Layout lay(p.d);
+template <typename T> int launch_norm_gate(const NormGateParams &q, cudaStream_t s) {
+    const NormGateParams p = divided(q);
     const int vec = pieces<T>({p.o, p.gate, p.out}, {p.d, p.o_sb, p.o_sh, p.o_sl, p.gate ? p.ldg : 0});
-    const int parts = gate_parts(lay, p, fwd_blocks(256), 1);
+    const Layout lay(p.d, true, vec);
+    const int parts = gate_parts(lay, p, true);
     const unsigned grid = (unsigned)parts * (p.per_head ? p.H : 1);
-    return with_layout<T>(lay, p.d, vec, [&](auto v, auto nc, auto mt) {
+    return with_layout<T, true>(lay, vec, [&](auto v, auto nc, auto mt) {
         constexpr int V = v(), N = nc(), M = mt();
         return p.gate ? launch<norm_gate_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 2, M>(lay.threads), ring_bytes<T, V, N, 2, M>(M), s, p, lay.tpr, parts)
                       : launch<norm_gate_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 1, M>(lay.threads), ring_bytes<T, V, N, 1, M>(M), s, p, lay.tpr, parts);
     });
 }
 
-template <typename T> int launch_norm_gate_bwd(const NormGateParams &p, cudaStream_t s) {
-    const Layout lay(p.d);
+template <typename T> int launch_norm_gate_bwd(const NormGateParams &q, cudaStream_t s) {
+    const NormGateParams p = divided(q);
+    const Layout lay(p.d, false);
     const int vec = pieces<T>({p.o, p.gate, p.dout, p.d_o, p.dgate},
                               {p.d, p.o_sb, p.o_sh, p.o_sl, p.do_sb, p.do_sh, p.do_sl, p.gate ? p.ldg : 0, p.gate ? p.lddg : 0});
-    const int parts = gate_parts(lay, p, bwd_blocks(256), kMinRows);
+    const int parts = gate_parts(lay, p, false);
     const unsigned grid = (unsigned)parts * (p.per_head ? p.H : 1);
-    with_layout<T>(lay, p.d, vec, [&](auto v, auto nc, auto mt) {
+    with_layout<T, false>(lay, vec, [&](auto v, auto nc, auto mt) {
         constexpr int V = v(), N = nc(), M = mt();
         return p.gate ? launch<norm_gate_bwd_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 3, M>(lay.threads), ring_bytes<T, V, N, 3, M>(M), s, p, lay.tpr, parts)
                       : launch<norm_gate_bwd_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 2, M>(lay.threads), ring_bytes<T, V, N, 2, M>(M), s, p, lay.tpr, parts);
     });
     if (!p.dweight) return 0;
     const long long n = (long long)p.d * (p.per_head ? p.H : 1);
-    sum_parts_kernel<<<(unsigned)((n + 31) / 32), 32 * kSegments, 0, s>>>(p.ws, parts, n, p.dweight, nullptr);
-    return 0;
+    return launch_sums(p.ws, parts, n, p.dweight, nullptr, s);
 }
 
 template <typename T> int launch_residual_norm(const ResidualNormParams &p, cudaStream_t s) {
-    const Layout lay(p.D);
     const int vec = pieces<T>({p.r, p.y, p.r_out, p.h}, {p.D});
-    const unsigned grid = (unsigned)lay.blocks(p.R, fwd_blocks(256), 1);
-    return with_layout<T>(lay, p.D, vec, [&](auto v, auto nc, auto mt) {
+    const Layout lay(p.D, true, vec);
+    const unsigned grid = (unsigned)lay.forward_blocks(p.R);
+    return with_layout<T, true>(lay, vec, [&](auto v, auto nc, auto mt) {
         constexpr int V = v(), N = nc(), M = mt();
         return p.y ? launch<residual_norm_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 2, M>(lay.threads), ring_bytes<T, V, N, 2, M>(M), s, p, lay.tpr)
                    : launch<residual_norm_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 1, M>(lay.threads), ring_bytes<T, V, N, 1, M>(M), s, p, lay.tpr);
@@ -699,17 +743,15 @@ template <typename T> int launch_residual_norm(const ResidualNormParams &p, cuda
 }
 
 template <typename T> int launch_residual_norm_bwd(const ResidualNormParams &p, cudaStream_t s) {
-    const Layout lay(p.D);
+    const Layout lay(p.D, false);
     const int vec = pieces<T>({p.r, p.y, p.dh, p.dr_out, p.dr, p.dy}, {p.D});
-    const unsigned grid = (unsigned)lay.blocks(p.R, bwd_blocks(256), kMinRows);
-    with_layout<T>(lay, p.D, vec, [&](auto v, auto nc, auto mt) {
+    const unsigned grid = (unsigned)lay.backward_blocks(p.R);
+    with_layout<T, false>(lay, vec, [&](auto v, auto nc, auto mt) {
         constexpr int V = v(), N = nc(), M = mt();
         return p.y ? launch<residual_norm_bwd_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 4, M>(lay.threads), ring_bytes<T, V, N, 4, M>(M), s, p, lay.tpr)
                    : launch<residual_norm_bwd_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 3, M>(lay.threads), ring_bytes<T, V, N, 3, M>(M), s, p, lay.tpr);
     });
-    if (p.dweight || p.dscale)
-        sum_parts_kernel<<<dim3((unsigned)((p.D + 31) / 32), p.dscale ? 2 : 1), 32 * kSegments, 0, s>>>(
-            p.ws, (int)grid, p.D, p.dweight, p.dscale);
+    if (p.dweight || p.dscale) return launch_sums(p.ws, (int)grid, p.D, p.dweight, p.dscale, s);
     return 0;
 }
 

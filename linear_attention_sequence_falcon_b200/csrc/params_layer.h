@@ -42,8 +42,15 @@ struct ScanStepParams {
     void *out;
 };
 
+// Division by a fixed number below 2^31 of numbers below 2^31: one product.
+struct FastDiv {
+    unsigned by, factor, shift;
+};
+
 struct NormGateParams {
     int B, H, L, d, per_head;
+    int small;                     // fewer than 2^31 rows: the divisions below hold
+    FastDiv heads, tokens;         // rows into (token, head), tokens into (b, l); set by the launcher
     long long o_sb, o_sh, o_sl, ldg;
     float eps;
     const void *o, *gate;          // gate may be NULL
