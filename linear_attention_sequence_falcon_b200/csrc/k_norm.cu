@@ -260,35 +260,30 @@ __device__ __forceinline__ unsigned divide(unsigned n, const FastDiv &f) {
     return f.by == 1 ? n : __umulhi(n, f.factor) >> (f.shift - 1);
 }
 
-struct GatePlace {
-    long long token;
-    int b, l, h;
-    // row `row` of the kernel's; `head`: the block's, or 0
-    __device__ __forceinline__ GatePlace(const NormGateParams &p, long long row, int head) {
-        if (p.small) {
-            const unsigned n = (unsigned)row, t = divide(n, p.heads);
-            token = t;
-            h = head + (int)(n - t * p.heads.by);
-            b = (int)divide(t, p.tokens);
-            l = (int)(t - (unsigned)b * p.tokens.by);
-        } else {
-            token = row / p.heads.by;
-            h = head + (int)(row - token * p.heads.by);
-            b = (int)(token / p.L);
-            l = (int)(token - (long long)b * p.L);
-        }
-    }
-    __device__ __forceinline__ long long strided(long long sb, long long sh, long long sl) const {
-        return b * sb + h * sh + l * sl;
-    }
-    __device__ __forceinline__ long long packed(const NormGateParams &p, long long ld) const {
-        return token * ld + (long long)h * p.d;
-    }
+// The offsets of a row's first channel in an array of strided rows (b*sb +
+// h*sh + l*sl), in one of tokens (ld apart) and in one of tokens without gaps.
+// Where all fit 31 bits (p.small), 32-bit arithmetic: a third of the instructions.
+struct GateOffsets {
+    long long strided, tokens, packed;
 };
-
-// the offset of a row in an array of tokens without gaps (out, dout)
-__device__ __forceinline__ long long packed_row(const NormGateParams &p, long long row, int head) {
-    return (p.per_head ? row * p.H + head : row) * p.d;
+// row `row` of the kernel's; `head`: the block's, or 0
+__device__ __forceinline__ GateOffsets gate_offsets(const NormGateParams &p, long long row, int head, long long sb,
+                                                    long long sh, long long sl, long long ld) {
+    GateOffsets r;
+    if (p.small) {
+        const unsigned n = (unsigned)row, token = divide(n, p.heads), h = head + (n - token * p.heads.by);
+        const unsigned b = divide(token, p.tokens), l = token - b * p.tokens.by;
+        r.strided = b * (unsigned)sb + h * (unsigned)sh + l * (unsigned)sl;
+        r.tokens = token * (unsigned)ld + h * (unsigned)p.d;
+        r.packed = (token * (unsigned)p.H + h) * (unsigned)p.d;
+    } else {
+        const long long token = row / p.heads.by, h = head + (row - token * p.heads.by);
+        const long long b = token / p.L, l = token - b * p.L;
+        r.strided = b * sb + h * sh + l * sl;
+        r.tokens = token * ld + h * p.d;
+        r.packed = (token * p.H + h) * p.d;
+    }
+    return r;
 }
 
 // Blocks per SM that the registers have to leave room for: threads up to 256,
@@ -310,9 +305,9 @@ __global__ void __launch_bounds__(MT, fwd_blocks(MT, VEC * NC)) norm_gate_kernel
     long long ahead = first + slot;
     auto fetch = [&](int stage) {
         const bool ok = ahead < end;
-        const GatePlace at(p, ok ? ahead : 0, head);
-        rows.fetch(stage, 0, static_cast<const T *>(p.o) + at.strided(p.o_sb, p.o_sh, p.o_sl), ok);
-        if constexpr (GATE) rows.fetch(stage, 1, static_cast<const T *>(p.gate) + at.packed(p, p.ldg), ok);
+        const GateOffsets at = gate_offsets(p, ok ? ahead : 0, head, p.o_sb, p.o_sh, p.o_sl, p.ldg);
+        rows.fetch(stage, 0, static_cast<const T *>(p.o) + at.strided, ok);
+        if constexpr (GATE) rows.fetch(stage, 1, static_cast<const T *>(p.gate) + at.tokens, ok);
         rows.close();
         ahead += step;
     };
@@ -338,7 +333,7 @@ __global__ void __launch_bounds__(MT, fwd_blocks(MT, VEC * NC)) norm_gate_kernel
             for (int e = 0; e < E; ++e) ov[e] *= zv[e] * sigmoid(zv[e]);
         }
         const long long row = base + slot;
-        if (row < end) rows.store(static_cast<T *>(p.out) + packed_row(p, row, head), ov);
+        if (row < end) rows.store(static_cast<T *>(p.out) + (p.per_head ? row * p.H + head : row) * d, ov);
         stage = Rows::next(stage);
     }
 }
@@ -357,10 +352,10 @@ __global__ void __launch_bounds__(MT, bwd_blocks(MT, VEC, VEC * NC)) norm_gate_b
     long long ahead = first + slot;
     auto fetch = [&](int stage) {
         const bool ok = ahead < end;
-        const GatePlace at(p, ok ? ahead : 0, head);
-        rows.fetch(stage, 0, static_cast<const T *>(p.o) + at.strided(p.o_sb, p.o_sh, p.o_sl), ok);
-        rows.fetch(stage, 1, static_cast<const T *>(p.dout) + packed_row(p, ok ? ahead : 0, head), ok);
-        if constexpr (GATE) rows.fetch(stage, 2, static_cast<const T *>(p.gate) + at.packed(p, p.ldg), ok);
+        const GateOffsets at = gate_offsets(p, ok ? ahead : 0, head, p.o_sb, p.o_sh, p.o_sl, p.ldg);
+        rows.fetch(stage, 0, static_cast<const T *>(p.o) + at.strided, ok);
+        rows.fetch(stage, 1, static_cast<const T *>(p.dout) + at.packed, ok);
+        if constexpr (GATE) rows.fetch(stage, 2, static_cast<const T *>(p.gate) + at.tokens, ok);
         rows.close();
         ahead += step;
     };
@@ -400,9 +395,9 @@ __global__ void __launch_bounds__(MT, bwd_blocks(MT, VEC, VEC * NC)) norm_gate_b
         }
         const long long row = base + slot;
         if (row < end) {
-            const GatePlace at(p, row, head);
-            rows.store(static_cast<T *>(p.d_o) + at.strided(p.do_sb, p.do_sh, p.do_sl), ov);
-            if constexpr (GATE) rows.store(static_cast<T *>(p.dgate) + at.packed(p, p.lddg), zv);
+            const GateOffsets at = gate_offsets(p, row, head, p.do_sb, p.do_sh, p.do_sl, p.lddg);
+            rows.store(static_cast<T *>(p.d_o) + at.strided, ov);
+            if constexpr (GATE) rows.store(static_cast<T *>(p.dgate) + at.tokens, zv);
         }
         stage = Rows::next(stage);
     }
@@ -570,14 +565,15 @@ __global__ void __launch_bounds__(32 * kSegments) sum_parts_kernel(const float *
 
 // How a row of d channels is laid on threads.  Backward: 8 channels a thread
 // (16 beyond 2048), so that the accumulators of the weights' gradients stay in
-// registers.  Forward there are none, and up to 1024 channels a row stays
-// inside a warp, which needs no barrier: up to 32 a thread (not in single
-// elements, whose loads are held in registers one by one).
+// registers.  Forward there are none: 16 beyond 64 channels, which halves what
+// a row costs beside its channels, and up to 1024 channels a row stays inside a
+// warp, which needs no barrier, with up to 32 (not in single elements, whose
+// loads are held in registers one by one).
 struct Layout {
     int each, tpr, threads, slots;
     Layout(int d, bool forward, int vec = 1) {
         each = d > 2048 ? 16 : 8;
-        if (forward && vec > 1 && d > 256 && d <= 1024) each = (d + 255) / 256 * 8;
+        if (forward && vec > 1 && d > 64 && d <= 1024) each = d <= 256 ? 16 : (d + 255) / 256 * 8;
         const int need = (d + each - 1) / each;
         if (need > 32) {
             tpr = (need + 31) / 32 * 32;
@@ -680,7 +676,14 @@ int gate_parts(const Layout &lay, const NormGateParams &p, bool forward) {
 NormGateParams divided(NormGateParams p) {
     p.heads = fast_div(p.per_head ? 1u : (unsigned)p.H);
     p.tokens = fast_div((unsigned)p.L);
-    p.small = (long long)p.B * p.L * p.heads.by < (1ll << 31);
+    const long long tokens = (long long)p.B * p.L, most = 1ll << 31;
+    auto strided = [&](long long sb, long long sh, long long sl) {
+        return (p.B - 1) * sb < most && (p.H - 1) * sh < most && (p.L - 1) * sl < most &&
+               (p.B - 1) * sb + (p.H - 1) * sh + (p.L - 1) * sl < most;
+    };
+    auto rows = [&](long long ld) { return tokens == 1 || (ld < most && tokens * ld < most); };
+    p.small = tokens < most / p.H / p.d && rows(p.ldg) && rows(p.lddg) && strided(p.o_sb, p.o_sh, p.o_sl) &&
+              strided(p.do_sb, p.do_sh, p.do_sl);
     return p;
 }
 

@@ -49,7 +49,7 @@ struct FastDiv {
 
 struct NormGateParams {
     int B, H, L, d, per_head;
-    int small;                     // fewer than 2^31 rows: the divisions below hold
+    int small;                     // fewer than 2^31 rows, every offset below 2^31: the divisions below hold
     FastDiv heads, tokens;         // rows into (token, head), tokens into (b, l); set by the launcher
     long long o_sb, o_sh, o_sl, ldg;
     float eps;
