@@ -82,7 +82,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) scan_kernel(
     __shared__ Cluster<LPR> cl;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, u = threadIdx.x / LPR;
     const int cs = (int)cluster_size(), rank = (int)cluster_rank();
+    extern __shared__ __align__(16) uint8_t dynamic[];
     cl.begin(cs);
+    float4 *const maps_of = reinterpret_cast<float4 *>(dynamic);  // the cluster's tiles' maps, [2][cs][LPR]
     const int groups = (p.D + G::kChannels - 1) / G::kChannels;
     const int unit_id = blockIdx.x / cs, n = unit_id / groups;
     const int ch0 = (unit_id % groups) * G::kChannels, ch = ch0 + (V ? 2 * l : l);
@@ -147,13 +149,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) scan_kernel(
             Map all = before;
             for (int i = u; i < G::kRuns; ++i) all = join<R>(load_map(&agg[par][i * LPR + l]), all);
             if (cs == 1) carry = apply<R>(all, h);
-            else if (lane < LPR) send(&cl.maps[par][rank][l], &cl.bar[par], warp, as4(all));
+            else
+                for (int to = warp; to < cs && lane < LPR; to += kThreads / 32)
+                    send(&maps_of[(par * cs + rank) * LPR + l], &cl.bar[par], to, as4(all));
         }
         if (cs > 1) {
             cl.wait(step);
-            for (int i = 0; i < rank; ++i) h = apply<R>(load_map(&cl.maps[par][i][l]), h);
+            for (int i = 0; i < rank; ++i) h = apply<R>(load_map(&maps_of[(par * cs + i) * LPR + l]), h);
             carry = h;
-            for (int i = rank; i < cs; ++i) carry = apply<R>(load_map(&cl.maps[par][i][l]), carry);
+            for (int i = rank; i < cs; ++i) carry = apply<R>(load_map(&maps_of[(par * cs + i) * LPR + l]), carry);
         }
         h = apply<R>(before, h);
         if (p.marks && u % G::kMark == 0 && t0 < p.L)
@@ -188,7 +192,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanBwdParams p) 
     __shared__ Cluster<LPR> cl;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, u = threadIdx.x / LPR;
     const int cs = (int)cluster_size(), rank = (int)cluster_rank();
+    extern __shared__ __align__(16) uint8_t dynamic[];
     cl.begin(cs);
+    float4 *const maps_of = reinterpret_cast<float4 *>(dynamic);  // the cluster's tiles' maps, [2][cs][LPR]
     const int groups = (p.D + G::kChannels - 1) / G::kChannels;
     const int unit_id = blockIdx.x / cs, n = unit_id / groups;
     const int ch0 = (unit_id % groups) * G::kChannels, ch = ch0 + (V ? 2 * l : l);
@@ -268,7 +274,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanBwdParams p) 
             Map all = behind;
             for (int i = u; i >= 0; --i) all = join<R>(load_map(&agg[par][i * LPR + l]), all);
             if (cs == 1) carry = apply<R>(all, y);
-            else if (lane < LPR) send(&cl.maps[par][rank][l], &cl.bar[par], warp, as4(all));
+            else
+                for (int to = warp; to < cs && lane < LPR; to += kThreads / 32)
+                    send(&maps_of[(par * cs + rank) * LPR + l], &cl.bar[par], to, as4(all));
         }
         // the state in front of this run, from the mark of its eight
         float2 h = mark;
@@ -286,9 +294,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanBwdParams p) 
         }
         if (cs > 1) {
             cl.wait(turn);
-            for (int i = cs - 1; i > rank; --i) y = apply<R>(load_map(&cl.maps[par][i][l]), y);
+            for (int i = cs - 1; i > rank; --i) y = apply<R>(load_map(&maps_of[(par * cs + i) * LPR + l]), y);
             carry = y;
-            for (int i = rank; i >= 0; --i) carry = apply<R>(load_map(&cl.maps[par][i][l]), carry);
+            for (int i = rank; i >= 0; --i) carry = apply<R>(load_map(&maps_of[(par * cs + i) * LPR + l]), carry);
         }
         y = apply<R>(behind, y);
         const bool whole = wide && tile0 + G::kTile <= p.L;
@@ -356,7 +364,7 @@ template <typename T> int launch_scan(const ScanParams &p, cudaStream_t s) {
         const long long units = (long long)p.N * ((p.D + G::kChannels - 1) / G::kChannels);
         return with_bools(v, p.reset != nullptr, [&](auto vv, auto rr) {
             return launch_units(scan_kernel<T, decltype(vv)::value, decltype(lpr)::value, decltype(rr)::value>,
-                                units, (p.L + G::kTile - 1) / G::kTile, kThreads, 0, s, p);
+                                units, (p.L + G::kTile - 1) / G::kTile, kThreads, 0, Cluster<decltype(lpr)::value>::kBytes, s, p);
         });
     });
 }
@@ -372,7 +380,7 @@ template <typename T> int launch_scan_bwd(const ScanBwdParams &p, cudaStream_t s
         const long long units = (long long)p.N * ((p.D + G::kChannels - 1) / G::kChannels);
         return with_bools(v, p.reset != nullptr, [&](auto vv, auto rr) {
             return launch_units(scan_bwd_kernel<T, decltype(vv)::value, decltype(lpr)::value, decltype(rr)::value>,
-                                units, (p.L + G::kTile - 1) / G::kTile, kThreads, 0, s, p);
+                                units, (p.L + G::kTile - 1) / G::kTile, kThreads, 0, Cluster<decltype(lpr)::value>::kBytes, s, p);
         });
     });
 }

@@ -42,13 +42,13 @@ struct BwdMaps {
 template <typename T, int A> struct Ring {
     static constexpr int S = kStages;
     static constexpr int kStage = A * tile_bytes<T>();
-    static constexpr size_t kBytes = (size_t)S * kStage + 128;
+    static constexpr size_t kBytes = (size_t)S * kStage;
     uint8_t *base;
     uint64_t *full;
     int issued;  // turns loaded so far (the loading thread's)
 
     __device__ __forceinline__ void begin(uint8_t *dynamic, uint64_t *bars) {
-        base = dynamic + ((128 - (tc::smem_u32(dynamic) & 127)) & 127);
+        base = dynamic;
         full = bars;
         issued = 0;
         if (threadIdx.x == 0) {
@@ -94,7 +94,7 @@ template <typename T, int A> struct Ring {
 template <typename T, bool R>
 __global__ void __launch_bounds__(kTmaThreads, sizeof(T) == 2 ? 4 : 3)
 scan_tma_kernel(const __grid_constant__ FwdMaps maps, ScanParams p) {
-    extern __shared__ uint8_t dynamic[];
+    extern __shared__ __align__(128) uint8_t dynamic[];
     __shared__ float4 agg[2][kTmaThreads];
     __shared__ Cluster<32> cl;
     __shared__ uint64_t bars[kStages];
@@ -105,6 +105,7 @@ scan_tma_kernel(const __grid_constant__ FwdMaps maps, ScanParams p) {
     Tiles ring;
     ring.begin(dynamic, bars);
     cl.begin(cs);
+    float4 *const maps_of = reinterpret_cast<float4 *>(dynamic + Tiles::kBytes);  // the cluster's tiles' maps, [2][cs][32]
     const int groups = (p.D + kCh - 1) / kCh;
     const int unit_id = blockIdx.x / cs, n = unit_id / groups;
     const int ch0 = (unit_id % groups) * kCh, ch = ch0 + 2 * lane;
@@ -157,11 +158,11 @@ scan_tma_kernel(const __grid_constant__ FwdMaps maps, ScanParams p) {
         if (cs == 1) {
             carry = apply<R>(all, h);
         } else {
-            for (int to = u; to < cs; to += kWarps) send(&cl.maps[par][rank][lane], &cl.bar[par], to, as4(all));
+            for (int to = u; to < cs; to += kWarps) send(&maps_of[(par * cs + rank) * 32 + lane], &cl.bar[par], to, as4(all));
             cl.wait(step);
-            for (int i = 0; i < rank; ++i) h = apply<R>(load_map(&cl.maps[par][i][lane]), h);
+            for (int i = 0; i < rank; ++i) h = apply<R>(load_map(&maps_of[(par * cs + i) * 32 + lane]), h);
             carry = h;
-            for (int i = rank; i < cs; ++i) carry = apply<R>(load_map(&cl.maps[par][i][lane]), carry);
+            for (int i = rank; i < cs; ++i) carry = apply<R>(load_map(&maps_of[(par * cs + i) * 32 + lane]), carry);
         }
         if (p.marks && u == 0 && left > 0 && in)
             store_pair<float, false>(p.marks + ((long long)n * tiles + step * cs + rank) * p.D + ch, 1, true, true, h);
@@ -187,7 +188,7 @@ scan_tma_kernel(const __grid_constant__ FwdMaps maps, ScanParams p) {
 template <typename T, bool R>
 __global__ void __launch_bounds__(kTmaThreads, sizeof(T) == 2 ? 3 : 2)
 scan_bwd_tma_kernel(const __grid_constant__ BwdMaps maps, ScanBwdParams p) {
-    extern __shared__ uint8_t dynamic[];
+    extern __shared__ __align__(128) uint8_t dynamic[];
     __shared__ float4 agg[2][kTmaThreads];  // product of the gates, y's map
     __shared__ float2 fwd[2][kTmaThreads];  // the state's B
     __shared__ Cluster<32> cl;
@@ -199,6 +200,7 @@ scan_bwd_tma_kernel(const __grid_constant__ BwdMaps maps, ScanBwdParams p) {
     Tiles ring;
     ring.begin(dynamic, bars);
     cl.begin(cs);
+    float4 *const maps_of = reinterpret_cast<float4 *>(dynamic + Tiles::kBytes);  // the cluster's tiles' maps, [2][cs][32]
     const int groups = (p.D + kCh - 1) / kCh;
     const int unit_id = blockIdx.x / cs, n = unit_id / groups;
     const int ch0 = (unit_id % groups) * kCh, ch = ch0 + 2 * lane;
@@ -262,7 +264,7 @@ scan_bwd_tma_kernel(const __grid_constant__ BwdMaps maps, ScanBwdParams p) {
         float2 y = carry;
         if (cs == 1) carry = apply<R>(all, y);
         else
-            for (int to = u; to < cs; to += kWarps) send(&cl.maps[par][rank][lane], &cl.bar[par], to, as4(all));
+            for (int to = u; to < cs; to += kWarps) send(&maps_of[(par * cs + rank) * 32 + lane], &cl.bar[par], to, as4(all));
         // the state in front of this run, from the tile's mark
 #pragma unroll
         for (int i = 0; i < kWarps - 1; ++i)
@@ -280,9 +282,9 @@ scan_bwd_tma_kernel(const __grid_constant__ BwdMaps maps, ScanBwdParams p) {
         }
         if (cs > 1) {
             cl.wait(turn);
-            for (int i = cs - 1; i > rank; --i) y = apply<R>(load_map(&cl.maps[par][i][lane]), y);
+            for (int i = cs - 1; i > rank; --i) y = apply<R>(load_map(&maps_of[(par * cs + i) * 32 + lane]), y);
             carry = y;
-            for (int i = rank; i >= 0; --i) carry = apply<R>(load_map(&cl.maps[par][i][lane]), carry);
+            for (int i = rank; i >= 0; --i) carry = apply<R>(load_map(&maps_of[(par * cs + i) * 32 + lane]), carry);
         }
         y = apply<R>(behind, y);
         const long long last = (long long)n * p.L + t0 + kRun - 1;
@@ -358,8 +360,8 @@ template <typename T> int launch_scan_tma(const ScanParams &p, cudaStream_t s) {
     const long long units = (long long)p.N * ((p.D + kCh - 1) / kCh);
     const int tiles = (p.L + kTile - 1) / kTile;
     constexpr size_t smem = Ring<T, 2>::kBytes;
-    return p.reset ? launch_units(scan_tma_kernel<T, true>, units, tiles, kTmaThreads, smem, s, maps, p)
-                   : launch_units(scan_tma_kernel<T, false>, units, tiles, kTmaThreads, smem, s, maps, p);
+    return p.reset ? launch_units(scan_tma_kernel<T, true>, units, tiles, kTmaThreads, smem, Cluster<32>::kBytes, s, maps, p)
+                   : launch_units(scan_tma_kernel<T, false>, units, tiles, kTmaThreads, smem, Cluster<32>::kBytes, s, maps, p);
 }
 
 template <typename T> int launch_scan_bwd_tma(const ScanBwdParams &p, cudaStream_t s) {
@@ -374,8 +376,8 @@ template <typename T> int launch_scan_bwd_tma(const ScanBwdParams &p, cudaStream
     const long long units = (long long)p.N * ((p.D + kCh - 1) / kCh);
     const int tiles = (p.L + kTile - 1) / kTile;
     constexpr size_t smem = Ring<T, 3>::kBytes;
-    return p.reset ? launch_units(scan_bwd_tma_kernel<T, true>, units, tiles, kTmaThreads, smem, s, maps, p)
-                   : launch_units(scan_bwd_tma_kernel<T, false>, units, tiles, kTmaThreads, smem, s, maps, p);
+    return p.reset ? launch_units(scan_bwd_tma_kernel<T, true>, units, tiles, kTmaThreads, smem, Cluster<32>::kBytes, s, maps, p)
+                   : launch_units(scan_bwd_tma_kernel<T, false>, units, tiles, kTmaThreads, smem, Cluster<32>::kBytes, s, maps, p);
 }
 
 unsigned int scan_tma_wait_timeouts() {

@@ -14,7 +14,7 @@
 namespace falcon {
 namespace scan {
 
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;  // beyond 8: not portable, allowed per kernel
 constexpr uint64_t kGiveUpNs = 2000000000ull;  // a wait for the cluster's maps
 
 
@@ -165,11 +165,11 @@ __device__ __forceinline__ bool wait_parity(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
-// The exchange of the tiles' maps inside a cluster.  Step s uses half s & 1 of
-// `maps`: a block sends step s + 2 only after every block's map of step s + 1
+// The exchange of the tiles' maps inside a cluster (shared by the block's
+// threads; the maps themselves are in dynamic memory).  Step s uses half s & 1: a block sends step s + 2 only after every block's map of step s + 1
 // has come, which each sends after its reads of step s.
 template <int LPR> struct Cluster {
-    float4 maps[2][kMaxCluster][LPR];
+    static constexpr size_t kBytes = 2 * LPR * sizeof(float4);  // of the maps [2][cs][LPR], per block of the cluster
     uint64_t bar[2];
     int gave_up;
 
@@ -252,6 +252,7 @@ template <typename K> int clusters_held(K kernel, int cs, int threads, size_t sm
     }
     if (slot && *slot) return *slot;
     if (smem > 0) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(cs * 148);
     c.blockDim = dim3(threads);
@@ -273,11 +274,13 @@ template <typename K> int clusters_held(K kernel, int cs, int threads, size_t sm
 // The cluster's size: blocks walk steps = tiles/cs tiles each, in as many
 // waves as the device needs for all units' clusters; the size with the least
 // waves x steps, the smallest of equals (a smaller cluster joins fewer maps).
-template <typename K> int pick_cluster(K kernel, long long units, int tiles, int threads, size_t smem) {
+// `smem_each`: shared memory for every block of the cluster, beside `smem`.
+template <typename K>
+int pick_cluster(K kernel, long long units, int tiles, int threads, size_t smem, size_t smem_each) {
     int best = 1;
     long long cost = 0;
     for (int cs = 1; cs <= kMaxCluster && cs <= tiles; ++cs) {
-        const int held = clusters_held(kernel, cs, threads, smem);
+        const int held = clusters_held(kernel, cs, threads, smem + cs * smem_each);
         const long long waves = (units + held - 1) / held;
         const long long here = waves * ((tiles + cs - 1) / cs);
         if (cs == 1 || here < cost) { best = cs; cost = here; }
@@ -286,12 +289,13 @@ template <typename K> int pick_cluster(K kernel, long long units, int tiles, int
 }
 
 template <typename K, typename... P>
-int launch_units(K kernel, long long units, int tiles, int threads, size_t smem, cudaStream_t s, const P &...p) {
-    const int cs = pick_cluster(kernel, units, tiles, threads, smem);
+int launch_units(K kernel, long long units, int tiles, int threads, size_t smem, size_t smem_each, cudaStream_t s,
+                 const P &...p) {
+    const int cs = pick_cluster(kernel, units, tiles, threads, smem, smem_each);
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)(units * cs));
     c.blockDim = dim3(threads);
-    c.dynamicSmemBytes = smem;
+    c.dynamicSmemBytes = smem + cs * smem_each;
     c.stream = s;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;

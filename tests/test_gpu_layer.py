@@ -212,8 +212,8 @@ def untouched(buf, start, n):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("offset", [0, 1, 3])
-@pytest.mark.parametrize("N,L,D", [(2, 130, 64), (1, 300, 67), (3, 20, 128)])
+@pytest.mark.parametrize("offset", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("N,L,D", [(2, 130, 64), (1, 300, 67), (3, 20, 128), (1, 700, 70), (2, 333, 18)])
 def test_scan_alignment_and_borders(F, N, L, D, offset, dtype):
     """Arrays that begin off any vector's boundary, and nothing written beside the outputs."""
     t = TYPES[dtype]
