@@ -339,12 +339,14 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanStepParams p) {
 
 // ---- launches
 
-// Lanes per run: the fewest that hold the row's pairs, 32 at most.
-template <typename F> int with_lanes(int D, F go) {
+// Lanes per run: the fewest that hold the row's pairs, 32 at most (fp32 alone:
+// k_scan_tile.cu has taken every other row of more than 32 channels).
+template <typename T, typename F> int with_lanes(int D, F go) {
     if (D <= 8) return go(std::integral_constant<int, 4>());
     if (D <= 16) return go(std::integral_constant<int, 8>());
-    if (D <= 32) return go(std::integral_constant<int, 16>());
-    return go(std::integral_constant<int, 32>());
+    if constexpr (sizeof(T) == 4)
+        if (D > 32) return go(std::integral_constant<int, 32>());
+    return go(std::integral_constant<int, 16>());
 }
 
 template <typename F> int with_bools(bool v, bool r, F go) {
@@ -355,11 +357,11 @@ template <typename F> int with_bools(bool v, bool r, F go) {
 }  // namespace
 
 template <typename T> int launch_scan(const ScanParams &p, cudaStream_t s) {
-    const int tma = launch_scan_tma<T>(p, s);
-    if (tma != 1) return tma;
+    const int tile = launch_scan_tile<T>(p, s);
+    if (tile != 1) return tile;
     const bool v = p.D % 2 == 0 && pair_aligned(p.x, sizeof(T), p.ldx) && pair_aligned(p.f, sizeof(T), p.ldf) &&
                    (!p.out || pair_aligned(p.out, sizeof(T), p.D));
-    return with_lanes(p.D, [&](auto lpr) {
+    return with_lanes<T>(p.D, [&](auto lpr) {
         using G = Place<decltype(lpr)::value, kRun>;
         const long long units = (long long)p.N * ((p.D + G::kChannels - 1) / G::kChannels);
         return with_bools(v, p.reset != nullptr, [&](auto vv, auto rr) {
@@ -370,12 +372,12 @@ template <typename T> int launch_scan(const ScanParams &p, cudaStream_t s) {
 }
 
 template <typename T> int launch_scan_bwd(const ScanBwdParams &p, cudaStream_t s) {
-    const int tma = launch_scan_bwd_tma<T>(p, s);
-    if (tma != 1) return tma;
+    const int tile = launch_scan_bwd_tile<T>(p, s);
+    if (tile != 1) return tile;
     const bool v = p.D % 2 == 0 && pair_aligned(p.x, sizeof(T), p.ldx) && pair_aligned(p.f, sizeof(T), p.ldf) &&
                    pair_aligned(p.dout, sizeof(T), p.D) && pair_aligned(p.dx, sizeof(T), p.lddx) &&
                    pair_aligned(p.df, sizeof(T), p.lddf);
-    return with_lanes(p.D, [&](auto lpr) {
+    return with_lanes<T>(p.D, [&](auto lpr) {
         using G = Place<decltype(lpr)::value, kRun>;
         const long long units = (long long)p.N * ((p.D + G::kChannels - 1) / G::kChannels);
         return with_bools(v, p.reset != nullptr, [&](auto vv, auto rr) {
@@ -398,7 +400,7 @@ template <typename T> int launch_scan_step(const ScanStepParams &p, cudaStream_t
 unsigned int scan_wait_timeouts() {
     unsigned int v = 0;
     cudaMemcpyFromSymbol(&v, g_scan_wait_timeouts, sizeof(v));
-    return v + scan_tma_wait_timeouts();
+    return v + scan_tile_wait_timeouts();
 }
 
 template int launch_scan<float>(const ScanParams &, cudaStream_t);

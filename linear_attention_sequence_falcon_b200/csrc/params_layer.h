@@ -79,11 +79,11 @@ struct ResidualNormParams {
 
 template <typename T> int launch_scan(const ScanParams &p, cudaStream_t s);
 template <typename T> int launch_scan_bwd(const ScanBwdParams &p, cudaStream_t s);
-// the same fed by TMA (k_scan_tma.cu): rows on 16-byte boundaries, more than
-// 32 channels; 1 (nothing launched) for what they do not cover
-template <typename T> int launch_scan_tma(const ScanParams &p, cudaStream_t s);
-template <typename T> int launch_scan_bwd_tma(const ScanBwdParams &p, cudaStream_t s);
-unsigned int scan_tma_wait_timeouts();
+// the same for more than 32 channels (k_scan_tile.cu): fp32 rows on 16-byte
+// boundaries, bf16 rows on any; 1 (nothing launched) for what they do not cover
+template <typename T> int launch_scan_tile(const ScanParams &p, cudaStream_t s);
+template <typename T> int launch_scan_bwd_tile(const ScanBwdParams &p, cudaStream_t s);
+unsigned int scan_tile_wait_timeouts();
 template <typename T> int launch_scan_step(const ScanStepParams &p, cudaStream_t s);
 template <typename T> int launch_norm_gate(const NormGateParams &p, cudaStream_t s);
 template <typename T> int launch_norm_gate_bwd(const NormGateParams &p, cudaStream_t s);

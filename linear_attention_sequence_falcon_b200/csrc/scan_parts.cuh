@@ -1,5 +1,5 @@
 // scan_parts.cuh -- what the kernels of the gated linear recurrence share
-// (k_scan.cu, k_scan_tma.cu): gates, pairs of channels, affine maps of the
+// (k_scan.cu, k_scan_tile.cu): gates, pairs of channels, affine maps of the
 // state, their exchange inside a cluster, and the choice of the cluster's size.
 #pragma once
 
@@ -78,8 +78,13 @@ __device__ __forceinline__ Raw<T> load_pair(const T *p, int gap, bool in0, bool 
     if constexpr (V) {
         if (in0) r.v = *reinterpret_cast<const decltype(r.v) *>(p);
     } else {
-        const float x = in0 ? to_f32(p[0]) : fill, y = in1 ? to_f32(p[gap]) : fill;
-        r.set(x, y);
+        if constexpr (sizeof(T) == 2) {
+            const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
+            const unsigned short f = __float_as_uint(fill) >> 16, x = in0 ? q[0] : f, y = in1 ? q[gap] : f;
+            r.v = (uint32_t)x | (uint32_t)y << 16;
+        } else {
+            r.v = make_float2(in0 ? p[0] : fill, in1 ? p[gap] : fill);
+        }
     }
     return r;
 }
