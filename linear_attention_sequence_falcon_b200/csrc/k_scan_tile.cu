@@ -195,7 +195,7 @@ scan_tile_kernel(const __grid_constant__ FwdMaps maps, ScanParams p) {
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             float2 a, c;
-            gates(ring.get(step, 1, i), a, c);
+            gates<sizeof(T) == 4>(ring.get(step, 1, i), a, c);
             const float2 b = mul2(c, ring.get(step, 0, i));
             const bool r = R && (cut >> i & 1);
             hl[i] = i == 0 || r ? b : fma2(a, hl[i - 1], b);
@@ -311,7 +311,7 @@ scan_bwd_tile_kernel(const __grid_constant__ BwdMaps maps, ScanBwdParams p) {
         if (left < kRun) ring.keep_behind(turn, left);
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            gates(ring.get(turn, 1, i), a[i], c[i]);
+            gates<true>(ring.get(turn, 1, i), a[i], c[i]);
             q[i] = mul2(c[i], ring.get(turn, 0, i));
             const bool r = R && (cut >> i & 1);
             hl = i == 0 || r ? q[i] : fma2(a[i], hl, q[i]);

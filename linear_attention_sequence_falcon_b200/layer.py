@@ -70,23 +70,15 @@ def _rows(t, name, shape, dtype, index):
     all its sequences evenly spaced."""
     if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
         _refuse(t, name, shape, dtype, index)
-    D = shape[-1]
-    if t.is_contiguous():
-        return D
-    st = t.stride()
-    if D > 1 and st[-1] != 1:
+    st, D = t.stride(), shape[-1]
+    if st[-1] != 1 and D > 1:
         raise FalconError("the last axis of %s must be contiguous" % name)
-    step, span = None, 1  # tokens covered by the axes seen so far, from the last one outwards
-    for i in range(len(shape) - 2, -1, -1):
-        n = shape[i]
-        if n == 1:
-            continue
-        if step is None:
-            step = st[i]
-        elif st[i] != step * span:
+    n, step = shape[0], st[0]  # [n, D], or [n, L, D] whose sequences follow at L rows
+    if len(shape) == 3 and shape[1] > 1:
+        step = st[1]
+        if n > 1 and st[0] != step * shape[1]:
             raise FalconError("the rows of %s must be evenly spaced (strides %s)" % (name, st))
-        span *= n
-    if step is None:
+    elif n <= 1:
         return D
     if step < D:
         raise FalconError("the rows of %s overlap (strides %s)" % (name, st))
