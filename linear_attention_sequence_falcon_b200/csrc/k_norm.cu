@@ -32,7 +32,8 @@ namespace falcon {
 namespace {
 
 constexpr int kSms = 148;
-constexpr int kMinRows = 4;     // rows that a block walks at least, where weights' gradients are wanted
+constexpr int kMinRows = 4;     // rows that a thread walks at least, where weights' gradients are wanted
+                                // and the device is full
 constexpr int kSegments = 32;   // partial sums joined side by side
 constexpr int kMaxRows = 3;     // rows of a thread in shared memory: the present one and two on their way
 
@@ -90,15 +91,18 @@ __device__ __forceinline__ void narrow(Piece<float, 1> &p, const float *f) { p.v
 
 // ---- a thread's pieces of the present row and of those to come, A arrays each:
 // S rows in shared memory (three where they fit the block's, whatever fits
-// otherwise), S - 1 of them on their way.  Two-byte pieces have no asynchronous
-// copy: the next row's are loaded into registers.  The widest fp32 rows have no
-// room at all (S = 0) and are read when used.
-template <typename T, int VEC, int NC, int A, int MT> struct Ahead {
+// otherwise), S - 1 of them on their way.  Of single elements the next row's are
+// loaded into registers: bf16 has no asynchronous copy of two bytes, and in fp32
+// copies of four took longer (16 against 14 us backward at 1003x1111).  The
+// widest fp32 rows have no room at all (S = 0) and are read when used.
+template <typename T, int VEC, int NC, int A, int MT, int BLOCKS> struct Ahead {
     using P = Piece<T, VEC>;
     static constexpr int kRow = A * NC * (int)sizeof(P);  // bytes per thread
-    static constexpr int kFit = 200 * 1024 / (MT * kRow);
-    static constexpr bool kHeld = sizeof(P) == 2;
-    static constexpr int S = kHeld ? 0 : kFit < kMaxRows ? kFit : kMaxRows;
+    // rows that fit BLOCKS blocks of an SM; two if one block can have them
+    static constexpr int kFit = 216 * 1024 / BLOCKS / (MT * kRow), kAlone = 200 * 1024 / (MT * kRow);
+    static constexpr int kRows = kFit >= 2 ? kFit : kAlone < 2 ? kAlone : 2;
+    static constexpr bool kHeld = VEC == 1;
+    static constexpr int S = kHeld ? 0 : kRows < kMaxRows ? kRows : kMaxRows;
     static constexpr int kAhead = S > 0 ? S - 1 : kHeld ? 1 : 0;
     static constexpr int kBytes = S * kRow;
     P *mine;
@@ -294,7 +298,7 @@ constexpr int bwd_blocks(int mt, int vec = 8, int each = 8) { return mt > 256 ? 
 template <typename T, int VEC, int NC, int MT, bool GATE>
 __global__ void __launch_bounds__(MT, fwd_blocks(MT, VEC * NC)) norm_gate_kernel(NormGateParams p, int tpr, int parts) {
     constexpr int E = VEC * NC;
-    using Rows = Ahead<T, VEC, NC, GATE ? 2 : 1, MT>;
+    using Rows = Ahead<T, VEC, NC, GATE ? 2 : 1, MT, fwd_blocks(MT, VEC * NC)>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][32][2];
     const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, d = p.d;
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(MT, fwd_blocks(MT, VEC * NC)) norm_gate_kernel
 template <typename T, int VEC, int NC, int MT, bool GATE>
 __global__ void __launch_bounds__(MT, bwd_blocks(MT, VEC, VEC * NC)) norm_gate_bwd_kernel(NormGateParams p, int tpr, int parts) {
     constexpr int E = VEC * NC;
-    using Rows = Ahead<T, VEC, NC, GATE ? 3 : 2, MT>;
+    using Rows = Ahead<T, VEC, NC, GATE ? 3 : 2, MT, bwd_blocks(MT, VEC, VEC * NC)>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][32][2];
     const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, d = p.d;
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(MT, bwd_blocks(MT, VEC, VEC * NC)) norm_gate_b
 template <typename T, int VEC, int NC, int MT, bool ADD>
 __global__ void __launch_bounds__(MT, fwd_blocks(MT, VEC * NC)) residual_norm_kernel(ResidualNormParams p, int tpr) {
     constexpr int E = VEC * NC;
-    using Rows = Ahead<T, VEC, NC, ADD ? 2 : 1, MT>;
+    using Rows = Ahead<T, VEC, NC, ADD ? 2 : 1, MT, fwd_blocks(MT, VEC * NC)>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][32][2];
     const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, d = p.D;
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(MT, fwd_blocks(MT, VEC * NC)) residual_norm_ke
 template <typename T, int VEC, int NC, int MT, bool ADD>
 __global__ void __launch_bounds__(MT, bwd_blocks(MT, VEC, VEC * NC)) residual_norm_bwd_kernel(ResidualNormParams p, int tpr) {
     constexpr int E = VEC * NC;
-    using Rows = Ahead<T, VEC, NC, ADD ? 4 : 3, MT>;
+    using Rows = Ahead<T, VEC, NC, ADD ? 4 : 3, MT, bwd_blocks(MT, VEC, VEC * NC)>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][32][2];
     const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, d = p.D;
@@ -564,16 +568,18 @@ __global__ void __launch_bounds__(32 * kSegments) sum_parts_kernel(const float *
 // ---- launches
 
 // How a row of d channels is laid on threads.  Backward: 8 channels a thread
-// (16 beyond 2048), so that the accumulators of the weights' gradients stay in
-// registers.  Forward there are none: 16 beyond 64 channels, which halves what
+// (16 beyond 2048, and in the gated norm, which has one weight to accumulate:
+// 30 against 27 us at 8x12x2048x64), so that the accumulators of the weights'
+// gradients stay in registers.  Forward there are none: 16 beyond 64 channels, which halves what
 // a row costs beside its channels, and up to 1024 channels a row stays inside a
 // warp, which needs no barrier, with up to 32 (not in single elements, whose
 // loads are held in registers one by one).
+enum Kind { kForward, kGateBackward, kResidualBackward };
 struct Layout {
     int each, tpr, threads, slots;
-    Layout(int d, bool forward, int vec = 1) {
-        each = d > 2048 ? 16 : 8;
-        if (forward && vec > 1 && d > 64 && d <= 1024) each = d <= 256 ? 16 : (d + 255) / 256 * 8;
+    Layout(int d, Kind kind, int vec = 1) {
+        each = d > 2048 || (kind == kGateBackward && vec > 1 && d > 32) ? 16 : 8;
+        if (kind == kForward && vec > 1 && d > 64 && d <= 1024) each = d <= 256 ? 16 : (d + 255) / 256 * 8;
         const int need = (d + each - 1) / each;
         if (need > 32) {
             tpr = (need + 31) / 32 * 32;
@@ -592,7 +598,11 @@ struct Layout {
         return (int)(want < (long long)kSms * held ? want : (long long)kSms * held);
     }
     int forward_blocks(long long rows) const { return blocks(rows, fwd_blocks(256, each), 1); }
-    int backward_blocks(long long rows) const { return blocks(rows, bwd_blocks(256, 8, each), kMinRows); }
+    // `all`: the rows of all heads
+    int backward_blocks(long long rows, long long all) const {
+        const long long fill = all / ((long long)slots * kSms);  // rows each, one block on every SM
+        return blocks(rows, bwd_blocks(256, 8, each), fill >= kMinRows ? kMinRows : fill > 1 ? (int)fill : 1);
+    }
 };
 
 bool vec_ok(const void *p) { return !p || (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -628,8 +638,8 @@ template <typename T, bool FORWARD, typename F> int with_layout(const Layout &la
 }
 
 // shared memory of a block of `threads`: the rows ahead; the block's sums use it later
-template <typename T, int VEC, int NC, int A, int MT> constexpr size_t ring_bytes(int threads) {
-    const size_t ring = (size_t)threads * Ahead<T, VEC, NC, A, MT>::kBytes, sums = (size_t)threads * VEC * NC * sizeof(float);
+template <typename T, int VEC, int NC, int A, int MT, int BLOCKS> constexpr size_t ring_bytes(int threads) {
+    const size_t ring = (size_t)threads * Ahead<T, VEC, NC, A, MT, BLOCKS>::kBytes, sums = (size_t)threads * VEC * NC * sizeof(float);
     return ring > sums ? ring : sums;
 }
 
@@ -665,8 +675,9 @@ int launch_sums(const float *part, int parts, long long n, float *out0, float *o
 
 // the blocks of the gated norm, per head where each stays with one
 int gate_parts(const Layout &lay, const NormGateParams &p, bool forward) {
-    auto blocks = [&](long long rows) { return forward ? lay.forward_blocks(rows) : lay.backward_blocks(rows); };
-    if (!p.per_head) return blocks((long long)p.B * p.L * p.H);
+    const long long every = (long long)p.B * p.L * p.H;
+    auto blocks = [&](long long rows) { return forward ? lay.forward_blocks(rows) : lay.backward_blocks(rows, every); };
+    if (!p.per_head) return blocks(every);
     // every head has blocks of its own: share the device's between them
     const int all = blocks((long long)p.B * p.L), share = (blocks(1ll << 60) + p.H - 1) / p.H;
     return all < share ? all : share;
@@ -690,44 +701,45 @@ NormGateParams divided(NormGateParams p) {
 }  // namespace
 
 size_t norm_gate_bwd_ws_bytes(int, int B, int H, int L, int d) {
-    const Layout lay(d, false);
+    // for any alignment, and weights of either kind
     NormGateParams p{};
     p.B = B; p.H = H; p.L = L;
     size_t most = 0;
-    for (p.per_head = 0; p.per_head < 2; ++p.per_head) {
-        const size_t n = (size_t)gate_parts(lay, p, false) * (p.per_head ? H : 1) * d;
-        most = n > most ? n : most;
-    }
+    for (int vec = 1; vec <= 2; ++vec)
+        for (p.per_head = 0; p.per_head < 2; ++p.per_head) {
+            const size_t n = (size_t)gate_parts(Layout(d, kGateBackward, vec), p, false) * (p.per_head ? H : 1) * d;
+            most = n > most ? n : most;
+        }
     return sizeof(float) * most;
 }
 size_t residual_norm_bwd_ws_bytes(int, int R, int D) {
-    return sizeof(float) * 2 * (size_t)Layout(D, false).backward_blocks(R) * D;
+    return sizeof(float) * 2 * (size_t)Layout(D, kResidualBackward).backward_blocks(R, R) * D;
 }
 
 template <typename T> int launch_norm_gate(const NormGateParams &q, cudaStream_t s) {
     const NormGateParams p = divided(q);
     const int vec = pieces<T>({p.o, p.gate, p.out}, {p.d, p.o_sb, p.o_sh, p.o_sl, p.gate ? p.ldg : 0});
-    const Layout lay(p.d, true, vec);
+    const Layout lay(p.d, kForward, vec);
     const int parts = gate_parts(lay, p, true);
     const unsigned grid = (unsigned)parts * (p.per_head ? p.H : 1);
     return with_layout<T, true>(lay, vec, [&](auto v, auto nc, auto mt) {
-        constexpr int V = v(), N = nc(), M = mt();
-        return p.gate ? launch<norm_gate_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 2, M>(lay.threads), ring_bytes<T, V, N, 2, M>(M), s, p, lay.tpr, parts)
-                      : launch<norm_gate_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 1, M>(lay.threads), ring_bytes<T, V, N, 1, M>(M), s, p, lay.tpr, parts);
+        constexpr int V = v(), N = nc(), M = mt(), B = fwd_blocks(M, V * N);
+        return p.gate ? launch<norm_gate_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 2, M, B>(lay.threads), ring_bytes<T, V, N, 2, M, B>(M), s, p, lay.tpr, parts)
+                      : launch<norm_gate_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 1, M, B>(lay.threads), ring_bytes<T, V, N, 1, M, B>(M), s, p, lay.tpr, parts);
     });
 }
 
 template <typename T> int launch_norm_gate_bwd(const NormGateParams &q, cudaStream_t s) {
     const NormGateParams p = divided(q);
-    const Layout lay(p.d, false);
     const int vec = pieces<T>({p.o, p.gate, p.dout, p.d_o, p.dgate},
                               {p.d, p.o_sb, p.o_sh, p.o_sl, p.do_sb, p.do_sh, p.do_sl, p.gate ? p.ldg : 0, p.gate ? p.lddg : 0});
+    const Layout lay(p.d, kGateBackward, vec);
     const int parts = gate_parts(lay, p, false);
     const unsigned grid = (unsigned)parts * (p.per_head ? p.H : 1);
     with_layout<T, false>(lay, vec, [&](auto v, auto nc, auto mt) {
-        constexpr int V = v(), N = nc(), M = mt();
-        return p.gate ? launch<norm_gate_bwd_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 3, M>(lay.threads), ring_bytes<T, V, N, 3, M>(M), s, p, lay.tpr, parts)
-                      : launch<norm_gate_bwd_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 2, M>(lay.threads), ring_bytes<T, V, N, 2, M>(M), s, p, lay.tpr, parts);
+        constexpr int V = v(), N = nc(), M = mt(), B = bwd_blocks(M, V, V * N);
+        return p.gate ? launch<norm_gate_bwd_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 3, M, B>(lay.threads), ring_bytes<T, V, N, 3, M, B>(M), s, p, lay.tpr, parts)
+                      : launch<norm_gate_bwd_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 2, M, B>(lay.threads), ring_bytes<T, V, N, 2, M, B>(M), s, p, lay.tpr, parts);
     });
     if (!p.dweight) return 0;
     const long long n = (long long)p.d * (p.per_head ? p.H : 1);
@@ -736,23 +748,23 @@ template <typename T> int launch_norm_gate_bwd(const NormGateParams &q, cudaStre
 
 template <typename T> int launch_residual_norm(const ResidualNormParams &p, cudaStream_t s) {
     const int vec = pieces<T>({p.r, p.y, p.r_out, p.h}, {p.D});
-    const Layout lay(p.D, true, vec);
+    const Layout lay(p.D, kForward, vec);
     const unsigned grid = (unsigned)lay.forward_blocks(p.R);
     return with_layout<T, true>(lay, vec, [&](auto v, auto nc, auto mt) {
-        constexpr int V = v(), N = nc(), M = mt();
-        return p.y ? launch<residual_norm_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 2, M>(lay.threads), ring_bytes<T, V, N, 2, M>(M), s, p, lay.tpr)
-                   : launch<residual_norm_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 1, M>(lay.threads), ring_bytes<T, V, N, 1, M>(M), s, p, lay.tpr);
+        constexpr int V = v(), N = nc(), M = mt(), B = fwd_blocks(M, V * N);
+        return p.y ? launch<residual_norm_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 2, M, B>(lay.threads), ring_bytes<T, V, N, 2, M, B>(M), s, p, lay.tpr)
+                   : launch<residual_norm_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 1, M, B>(lay.threads), ring_bytes<T, V, N, 1, M, B>(M), s, p, lay.tpr);
     });
 }
 
 template <typename T> int launch_residual_norm_bwd(const ResidualNormParams &p, cudaStream_t s) {
-    const Layout lay(p.D, false);
+    const Layout lay(p.D, kResidualBackward);
     const int vec = pieces<T>({p.r, p.y, p.dh, p.dr_out, p.dr, p.dy}, {p.D});
-    const unsigned grid = (unsigned)lay.backward_blocks(p.R);
+    const unsigned grid = (unsigned)lay.backward_blocks(p.R, p.R);
     with_layout<T, false>(lay, vec, [&](auto v, auto nc, auto mt) {
-        constexpr int V = v(), N = nc(), M = mt();
-        return p.y ? launch<residual_norm_bwd_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 4, M>(lay.threads), ring_bytes<T, V, N, 4, M>(M), s, p, lay.tpr)
-                   : launch<residual_norm_bwd_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 3, M>(lay.threads), ring_bytes<T, V, N, 3, M>(M), s, p, lay.tpr);
+        constexpr int V = v(), N = nc(), M = mt(), B = bwd_blocks(M, V, V * N);
+        return p.y ? launch<residual_norm_bwd_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 4, M, B>(lay.threads), ring_bytes<T, V, N, 4, M, B>(M), s, p, lay.tpr)
+                   : launch<residual_norm_bwd_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 3, M, B>(lay.threads), ring_bytes<T, V, N, 3, M, B>(M), s, p, lay.tpr);
     });
     if (p.dweight || p.dscale) return launch_sums(p.ws, (int)grid, p.D, p.dweight, p.dscale, s);
     return 0;

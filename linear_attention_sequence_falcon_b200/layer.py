@@ -104,11 +104,16 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _new(t, shape):
+    """A new contiguous array of this shape (t's number of elements), dtype and device."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(shape)  # empty_like: 0.6 us less
+
+
 def _workspace(need, workspace, like):
     if need == 0:
         return None, 0
     if workspace is None:
-        return like.new_empty(need, dtype=torch.uint8), need
+        return like.new_empty(need // like.element_size() + 1), need
     if workspace.device != like.device or not workspace.is_contiguous():
         raise FalconError("workspace must be a contiguous array on %s" % (like.device,))
     have = workspace.numel() * workspace.element_size()
@@ -177,7 +182,7 @@ def scan(x, f, reset=None, initial_state=None, out=None, final_state=None, marks
         with _on(x, stream):
             return scan(x, f, reset, initial_state, out, final_state, marks, want_state, want_marks)
     if out is None:
-        out = x.new_empty((N, L, D))
+        out = _new(x, x.shape)
     if final_state is None and want_state:
         final_state = x.new_empty((N, D), dtype=_F32)
     if marks is None and want_marks:
@@ -209,9 +214,9 @@ def scan_bwd(x, f, dout, dstate=None, reset=None, initial_state=None, marks=None
         with _on(x, stream):
             return scan_bwd(x, f, dout, dstate, reset, initial_state, marks, dx, df, None, workspace)
     if dx is None:
-        dx = x.new_empty((N, L, D))
+        dx = _new(x, x.shape)
     if df is None:
-        df = x.new_empty((N, L, D))
+        df = _new(f, x.shape)
     dinitial = x.new_empty((N, D), dtype=_F32)
     ws, have = None, 0
     if marks is None:
@@ -244,7 +249,7 @@ def scan_step(x, f, state, state_out=None, out=None, stream=None):
         with _on(x, stream):
             return scan_step(x, f, state, state_out, out)
     if out is None:
-        out = x.new_empty(shape)
+        out = _new(x, shape)
     _check(load().falcon_scan_step(dt, x.data_ptr(), f.data_ptr(), state.data_ptr(), N, D, ldx, ldf,
                                    state_out.data_ptr(), out.data_ptr(), _raw_stream(at)))
     return out, state_out
@@ -298,7 +303,7 @@ def norm_gate(o, gate, weight, eps: float, out=None, stream=None):
         with _on(o, stream):
             return norm_gate(o, gate, weight, eps, out)
     if out is None:
-        out = o.new_empty((B, L, H * d))
+        out = o.new_empty((B, L, H * d)) if gate is None else _new(gate, gate.shape)
     sb, sh, sl, _ = o.stride()
     _check(load().falcon_norm_gate(DTYPES[o.dtype], o.data_ptr(), sb, sh, sl, _p(gate), ldg, _p(weight),
                                    weight is not None and weight.dim() == 2, eps, B, H, L, d, out.data_ptr(),
@@ -333,9 +338,9 @@ def norm_gate_bwd(o, gate, weight, eps: float, dout, do=None, dgate=None, want_d
         with _on(o, stream):
             return norm_gate_bwd(o, gate, weight, eps, dout, do, dgate, want_dweight, None, workspace)
     if do is None:
-        do = o.new_empty((B, H, L, d))
+        do = _new(o, o.shape)
     if dgate is None and gate is not None:
-        dgate = o.new_empty((B, L, H * d))
+        dgate = _new(gate, gate.shape)
     dweight = torch.empty_like(weight) if weight is not None and want_dweight else None
     ws, have = _workspace(norm_gate_bwd_workspace_size(o.dtype, B, H, L, d), workspace, o)
     sb, sh, sl, _ = o.stride()
