@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) scan_kernel(
 #pragma unroll
         for (int i = 0; i < RUN; ++i) {
             float2 a, c;
-            gates<sizeof(T) == 4>(rf[i].f(), a, c);
+            gates<T>(rf[i].f(), a, c);
             const float2 b = mul2(c, rx[i].f());
             const bool r = R && (cut >> i & 1);
             hl[i] = i == 0 || r ? b : fma2(a, hl[i - 1], b);
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanBwdParams p) 
         float2 pa, hl, yl = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < RUN; ++i) {
-            gates<true>(rf[i].f(), a[i], c[i]);
+            gates<T>(rf[i].f(), a[i], c[i]);
             q[i] = mul2(c[i], rx[i].f());
             dy[i] = rd[i];
             const bool r = R && (cut >> i & 1);
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanStepParams p) {
     const float2 f = load_pair<T, V>(static_cast<const T *>(p.f) + n * p.ldf + ch, 1, true, in1, 0.f).f();
     const float2 s = load_pair<float, V>(p.state + at, 1, true, in1, 0.f).f();
     float2 a, c;
-    gates<true>(f, a, c);
+    gates<T>(f, a, c);
     const float2 h = fma2(a, s, mul2(c, x));
     store_pair<float, V>(p.state_out + at, 1, true, in1, h);
     store_pair<T, V>(static_cast<T *>(p.out) + at, 1, true, in1, h);

@@ -195,7 +195,7 @@ scan_tile_kernel(const __grid_constant__ FwdMaps maps, ScanParams p) {
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             float2 a, c;
-            gates<sizeof(T) == 4>(ring.get(step, 1, i), a, c);
+            gates<T>(ring.get(step, 1, i), a, c);
             const float2 b = mul2(c, ring.get(step, 0, i));
             const bool r = R && (cut >> i & 1);
             hl[i] = i == 0 || r ? b : fma2(a, hl[i - 1], b);
@@ -231,15 +231,18 @@ scan_tile_kernel(const __grid_constant__ FwdMaps maps, ScanParams p) {
             store_pair<float, false>(p.marks + ((long long)n * tiles + step * cs + rank) * p.D + ch, gap, in0, in1, h);
         h = apply<R>(before, h);
         if (!p.out) continue;
-        T *out = static_cast<T *>(p.out) + ((long long)n * p.L + t0) * p.D + ch;
+        // stores at 32-bit offsets from the tile's first row (strides are at most 2^21)
+        char *const out = static_cast<char *>(p.out) + ((long long)n * p.L + tile0) * p.D * (int)sizeof(T);
+        const uint32_t pitch = (uint32_t)p.D * (uint32_t)sizeof(T);
+        uint32_t at = (uint32_t)(u * kRun) * pitch + (uint32_t)ch * (uint32_t)sizeof(T);
         if (in1 && left >= kRun) {
 #pragma unroll
-            for (int i = 0; i < kRun; ++i, out += p.D)
-                store_pair<T, V>(out, gap, true, true, R && i >= first ? hl[i] : fma2(pa[i], h, hl[i]));
+            for (int i = 0; i < kRun; ++i, at += pitch)
+                store_pair<T, V>(reinterpret_cast<T *>(out + at), gap, true, true, R && i >= first ? hl[i] : fma2(pa[i], h, hl[i]));
         } else if (in0) {
 #pragma unroll
-            for (int i = 0; i < kRun; ++i, out += p.D)
-                store_pair<T, V>(out, gap, i < left, i < left && in1, R && i >= first ? hl[i] : fma2(pa[i], h, hl[i]));
+            for (int i = 0; i < kRun; ++i, at += pitch)
+                store_pair<T, V>(reinterpret_cast<T *>(out + at), gap, i < left, i < left && in1, R && i >= first ? hl[i] : fma2(pa[i], h, hl[i]));
         }
     }
     if (p.final_state && rank == 0 && u == 0)
@@ -311,7 +314,7 @@ scan_bwd_tile_kernel(const __grid_constant__ BwdMaps maps, ScanBwdParams p) {
         if (left < kRun) ring.keep_behind(turn, left);
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            gates<true>(ring.get(turn, 1, i), a[i], c[i]);
+            gates<T>(ring.get(turn, 1, i), a[i], c[i]);
             q[i] = mul2(c[i], ring.get(turn, 0, i));
             const bool r = R && (cut >> i & 1);
             hl = i == 0 || r ? q[i] : fma2(a[i], hl, q[i]);
@@ -360,15 +363,19 @@ scan_bwd_tile_kernel(const __grid_constant__ BwdMaps maps, ScanBwdParams p) {
             for (int i = rank; i >= 0; --i) carry = apply<R>(load_map(&maps_of[((par) * cs + i) * 32 + lane]), carry);
         }
         y = apply<R>(behind, y);
-        const long long last = (long long)n * p.L + t0 + kRun - 1;
-        T *dx = static_cast<T *>(p.dx) + last * p.lddx + ch, *df = static_cast<T *>(p.df) + last * p.lddf + ch;
+        const long long row0 = (long long)n * p.L + tile0;
+        char *const dx = static_cast<char *>(p.dx) + row0 * p.lddx * (int)sizeof(T);
+        char *const df = static_cast<char *>(p.df) + row0 * p.lddf * (int)sizeof(T);
+        const uint32_t px = (uint32_t)p.lddx * (uint32_t)sizeof(T), pf = (uint32_t)p.lddf * (uint32_t)sizeof(T);
+        const uint32_t last = u * kRun + kRun - 1;
+        uint32_t at_x = last * px + (uint32_t)ch * (uint32_t)sizeof(T), at_f = last * pf + (uint32_t)ch * (uint32_t)sizeof(T);
         auto finish = [&](auto whole) {
 #pragma unroll
-            for (int i = kRun - 1; i >= 0; --i, dx -= p.lddx, df -= p.lddf) {
+            for (int i = kRun - 1; i >= 0; --i, at_x -= px, at_f -= pf) {
                 const float2 g = add2(ring.get(turn, 2, i), y);
                 const bool here = whole() || i < left;
-                store_pair<T, V>(dx, gap, here, here && (whole() || in1), mul2(g, c[i]));
-                store_pair<T, V>(df, gap, here, here && (whole() || in1), mul2(g, q[i]));
+                store_pair<T, V>(reinterpret_cast<T *>(dx + at_x), gap, here, here && (whole() || in1), mul2(g, c[i]));
+                store_pair<T, V>(reinterpret_cast<T *>(df + at_f), gap, here, here && (whole() || in1), mul2(g, q[i]));
                 y = R && (cut >> i & 1) ? make_float2(0.f, 0.f) : mul2(a[i], g);
             }
         };

@@ -42,21 +42,33 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     return y;
 }
 
-// a = sigmoid(f), c = 1 - a, each to full relative accuracy, without a branch
-// on f's sign: e = exp(-f), a = 1/(1+e), c = e a.  The exponent is held at
-// 115 (f = -79.7: a is 2e-35 from there on), so that e a stays finite.
+// a = sigmoid(f), c = 1 - a.
 //
-// FINE: one Newton step on the reciprocal's last bit.  A gradient through a
-// thousand tokens is a product of as many a's: without the step the initial
-// state's is off by 6e-7 to 9e-7, with it by 3e-7.  bf16 forward goes without
-// (its state is off by 1.4e-7, its outputs by their rounding).
-template <bool FINE> __device__ __forceinline__ void gates(float2 f, float2 &a, float2 &c) {
-    const float2 z = mul2(f, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-    const float2 e = make_float2(ex2(min_nan(z.x, 115.f)), ex2(min_nan(z.y, 115.f)));
-    const float2 s = add2(e, make_float2(1.f, 1.f));
-    a = make_float2(rcp(s.x), rcp(s.y));
-    if constexpr (FINE) a = make_float2(fmaf(a.x, fmaf(-s.x, a.x, 1.f), a.x), fmaf(a.y, fmaf(-s.y, a.y, 1.f), a.y));
-    c = mul2(e, a);
+// fp32: each to full relative accuracy, without a branch on f's sign: e =
+// exp(-f), a = 1/(1+e), c = e a.  The exponent is held at 115 (f = -79.7: a is
+// 2e-35 from there on), so that e a stays finite; one Newton step takes the
+// reciprocal's last bit, since a gradient through a thousand tokens is a
+// product of as many a's (the initial state's was off by 6e-7 to 9e-7, with the
+// step by 3e-7).
+// bf16: c = 1/(1+exp(f)) to full relative accuracy, a = 1 - c rounded once, so
+// off by 2^-25 at most.  Where a is near 1, and products of it are long, that
+// is its last bit; where it is small it is small beside c x.  A third of the
+// instructions less.
+template <typename T> __device__ __forceinline__ void gates(float2 f, float2 &a, float2 &c) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float2 one = make_float2(1.f, 1.f);
+    if constexpr (sizeof(T) == 2) {
+        const float2 z = mul2(f, make_float2(kLog2e, kLog2e)), s = add2(make_float2(ex2(z.x), ex2(z.y)), one);
+        c = make_float2(rcp(s.x), rcp(s.y));
+        a = make_float2(1.f - c.x, 1.f - c.y);
+    } else {
+        const float2 z = mul2(f, make_float2(-kLog2e, -kLog2e));
+        const float2 e = make_float2(ex2(min_nan(z.x, 115.f)), ex2(min_nan(z.y, 115.f)));
+        const float2 s = add2(e, one);
+        a = make_float2(rcp(s.x), rcp(s.y));
+        a = make_float2(fmaf(a.x, fmaf(-s.x, a.x, 1.f), a.x), fmaf(a.y, fmaf(-s.y, a.y, 1.f), a.y));
+        c = mul2(e, a);
+    }
 }
 
 // ---- loads and stores of one thread's two channels (V: next to each other
