@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) scan_kernel(
         }
         agg[par][threadIdx.x] = as4({pa[RUN - 1], hl[RUN - 1]});
         fetch(step + 1);
+        settle(carry);
         __syncthreads();
         if (cs > 1 && cl.gave_up) break;
         // the map in front of this run, and, for those who pass it on, the tile's
@@ -264,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanBwdParams p) 
         agg[par][threadIdx.x] = as4({pa, yl});
         fwd[par][threadIdx.x] = hl;
         if constexpr (kAhead) fetch(step - 1);
+        settle(carry);
         __syncthreads();
         if (cs > 1 && cl.gave_up) break;
         // y's map behind this run, and, for those who pass it on, the tile's

@@ -207,6 +207,7 @@ scan_tile_kernel(const __grid_constant__ FwdMaps maps, ScanParams p) {
             const int t1 = t0 + cs * kTile;
             rr = reset_bits<32, kRun>(p.reset, (long long)n * p.L + t1, p.L - t1, lane);
         }
+        settle(carry);
         __syncthreads();
         if (cl.gave_up) break;
         if constexpr (FEED == kTensor) load(step + S);
@@ -325,6 +326,7 @@ scan_bwd_tile_kernel(const __grid_constant__ BwdMaps maps, ScanBwdParams p) {
         agg[par][threadIdx.x] = as4({pa, yl});
         fwd[par][threadIdx.x] = hl;
         ahead(step - 1);
+        settle(carry);
         __syncthreads();
         if (cl.gave_up) break;
         // every thread has left the tile of the turn before: its place takes the next but S - 1

@@ -233,6 +233,11 @@ template <int LPR> struct Cluster {
     }
 };
 
+// The state given has been read (its load is complete) before what follows: the
+// state left may be written to the same place, by another thread or block, once
+// all of them have passed the barrier or the exchange behind this.
+__device__ __forceinline__ void settle(float2 v) { asm volatile("" ::"f"(v.x), "f"(v.y) : "memory"); }
+
 // Which of the run's RUN tokens begin a document, as bits; the LPR lanes of
 // a run look at its bytes together.
 template <int LPR, int RUN>

@@ -523,6 +523,39 @@ def test_two_graphs_share_nothing(F):
             assert all(torch.equal(p, q) for p, q in zip(layer_calls(F, a), got)), turn
 
 
+FIRST_CALL = """
+import torch
+import linear_attention_sequence_falcon_b200 as F
+g = torch.Generator(device="cuda").manual_seed(3)
+x, f, d = (torch.randn(2, 200, 96, device="cuda", generator=g).bfloat16() for _ in range(3))
+w = torch.ones(48, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+def calls():
+    out, state, marks = F.scan(x, f, want_marks=True)
+    b = F.scan_bwd(x, f, d, marks=marks)
+    o = out.view(2, 200, 2, 48).transpose(1, 2)
+    n = F.norm_gate_bwd(o, f, w, 1e-6, d)
+    r = F.residual_norm(x, None, 1e-6, y=F.norm_gate(o, f, w, 1e-6))
+    return [out, state, b["df"], n["dweight"], n["do"], r[1]]
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, calls()))
+"""
+
+
+def test_first_call_is_captured(F):
+    """A process whose first calls are captured into a graph (nothing warmed up)."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 # ---------------------------------------------------------------- the operators together
 
 def test_layer_forward_backward(F):
