@@ -719,6 +719,64 @@ def run_backward(args):
         print(json.dumps(line), flush=True)
 
 
+def layer_rows(F, flush, steps):
+    """The operators of the layer around the update, on the shapes of
+    workloads 2 and 5 and of the decode (bf16): (name, bytes that have to be
+    read and written, the call)."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(20260201)
+    new = lambda *s, dtype=torch.bfloat16: torch.randn(s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    hbm, _, src = peaks()
+    rows = []
+
+    def row(name, nbytes, call):
+        t = time_call(call, flush, steps)
+        gbs = nbytes / (t / 1e3) / 1e9
+        rows.append({"layer": name, "ms": t, "dtype": "bf16",
+                     "roofline": {"bound": "hbm", "achieved": gbs, "peak": hbm, "unit": "GB/s", "frac": gbs / hbm,
+                                  "peak_source": src, "algorithmic_bytes_per_launch": nbytes}})
+
+    for B, H, L, d in ((8, 12, 2048, 64), (2, 16, 32768, 128)):
+        D, tok = H * d, B * L
+        e, shape = tok * D, "%dx%dx%d" % (B, L, D)
+        both = new(B, L, 2 * D)
+        both[..., D:] += 3.0  # gates that remember some twenty tokens
+        x, f, dout, h0 = both[..., :D], both[..., D:], new(B, L, D), new(B, D, dtype=torch.float32)
+        w, s = torch.ones(D, device="cuda"), torch.full((D,), 0.5, device="cuda")
+        out, state, marks = F.scan(x, f, initial_state=h0, want_marks=True)
+        dx, df = torch.empty_like(out), torch.empty_like(out)
+        row("scan " + shape, 6 * e + 8 * B * D,
+            lambda: F.scan(x, f, initial_state=h0, out=out, final_state=state, marks=marks, want_marks=True))
+        row("scan_bwd " + shape, 10 * e + 4 * B * D,
+            lambda: F.scan_bwd(x, f, dout, initial_state=h0, marks=marks, dx=dx, df=df))
+        o, do = new(B, H, L, d), torch.empty((B, H, L, d), dtype=torch.bfloat16, device="cuda")
+        heads = "%dx%dx%dx%d" % (B, H, L, d)
+        row("norm_gate " + heads, 6 * e, lambda: F.norm_gate(o, dout, w[:d], 1e-6, out=out))
+        row("norm_gate_bwd " + heads, 10 * e,
+            lambda: F.norm_gate_bwd(o, dout, w[:d], 1e-6, out, do=do, dgate=dx))
+        r = new(B, L, D)
+        row("residual_norm %dx%d" % (tok, D), 8 * e, lambda: F.residual_norm(r, w, 1e-6, y=dout, scale=s, r_out=out, h=dx))
+        row("residual_norm_bwd %dx%d" % (tok, D), 12 * e,
+            lambda: F.residual_norm_bwd(r, w, 1e-6, dx, dr_out=out, y=dout, scale=s, dr=df, dy=do.view(B, L, D)))
+        del both, x, f, dout, out, marks, dx, df, o, do, r
+    N, D = 64, 2048
+    both, st, one = new(N, 2 * D), new(N, D, dtype=torch.float32), torch.empty((N, D), dtype=torch.bfloat16, device="cuda")
+    row("scan_step %dx%d" % (N, D), N * D * 14, lambda: F.scan_step(both[:, :D], both[:, D:], st, out=one))
+    return rows
+
+
+def run_layer(args):
+    """--layer: layer_rows as one JSON line each.  Not the contract line."""
+    import torch
+    import linear_attention_sequence_falcon_b200 as F
+    from linear_attention_sequence_falcon_b200 import build
+    build.build()
+    F.load()
+    flush = torch.empty(256 * 1024 * 1024, dtype=torch.uint8, device="cuda")
+    for r in layer_rows(F, flush, args.steps):
+        print(json.dumps(r), flush=True)
+
+
 def workload_oracle_rate(d, variant, form, w):
     """The fp64 oracle in the row's own form -- the recurrent form for masked
     rows, whose O(L^2) oracle takes 7-80 s per (b,h) unit at L = 2048 -- on
@@ -770,11 +828,15 @@ def main():
                     help="with --backward: the form whose derivative is taken")
     ap.add_argument("--chunk-sweep", action="store_true",
                     help="the chunk form of workload 2 at chunk 16/32/64 and both pairings (one line each)")
+    ap.add_argument("--layer", action="store_true",
+                    help="time the layer operators: the gated recurrence, the gated norm, the residual norm")
     ap.add_argument("--profile", action="store_true",
                     help="run only warmup+steps device steps (no flush, e2e, clocks or JSON), for ncu")
     args = ap.parse_args()
     if args.chunk_sweep:
         return run_chunk_sweep(args)
+    if args.layer:
+        return run_layer(args)
     if args.backward:
         return run_backward(args)
     if args.workloads:
