@@ -299,9 +299,14 @@ template <typename K> int clusters_held(K kernel, int cs, int threads, size_t sm
     return held;
 }
 
-// The cluster's size: blocks walk steps = tiles/cs tiles each, in as many
-// waves as the device needs for all units' clusters; the size with the least
-// waves x steps, the smallest of equals (a smaller cluster joins fewer maps).
+// The cluster's size: blocks walk steps = tiles/cs tiles each, in as many waves
+// as the device needs for all units' clusters.  A step takes a latency (its
+// exchange) and a share of the SM that grows with the blocks on it, a wave its
+// start: waves x (steps x (1.5 + blocks per SM) + 4.5) fits what was measured
+// over sizes 1 to 16 of six shapes; the least, the smallest size of equals.
+// Least waves x steps took 5 for the forward pass at 8x2048x768 (21.1 us; 4
+// takes 19.3); without the waves' start the backward pass at 16x1024x1024 took
+// 16 (69 us; 3 takes 39).
 // `smem_each`: shared memory for every block of the cluster, beside `smem`.
 template <typename K>
 int pick_cluster(K kernel, long long units, int tiles, int threads, size_t smem, size_t smem_each) {
@@ -310,7 +315,8 @@ int pick_cluster(K kernel, long long units, int tiles, int threads, size_t smem,
     for (int cs = 1; cs <= kMaxCluster && cs <= tiles; ++cs) {
         const int held = clusters_held(kernel, cs, threads, smem + cs * smem_each);
         const long long waves = (units + held - 1) / held;
-        const long long here = waves * ((tiles + cs - 1) / cs);
+        const long long blocks = (units < held ? units : held) * cs;  // at once
+        const long long here = waves * ((tiles + cs - 1) / cs * (3 * 148 + 2 * blocks) + 9 * 148);
         if (cs == 1 || here < cost) { best = cs; cost = here; }
     }
     return best;
