@@ -213,19 +213,26 @@ scan_tile_kernel(const __grid_constant__ FwdMaps maps, ScanParams p) {
         if constexpr (FEED == kTensor) load(step + S);
         // the map in front of this run, and the tile's
         Map before = unit(), all = load_map(&agg[par][lane]);
+        if (u > 0) {  // the branches are the warp's
+            before = all;
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) {
-            if (i == u) before = all;
-            all = join<R>(load_map(&agg[par][i * 32 + lane]), all);
+            for (int i = 1; i < kWarps - 1; ++i)
+                if (i < u) before = join<R>(load_map(&agg[par][i * 32 + lane]), before);
+            all = join<R>({pa[kRun - 1], hl[kRun - 1]}, before);
         }
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i)
+            if (i > u) all = join<R>(load_map(&agg[par][i * 32 + lane]), all);
         float2 h = carry;
         if (cs == 1) {
             carry = apply<R>(all, h);
         } else {
             for (int to = u; to < cs; to += kWarps) send(&maps_of[((par) * cs + rank) * 32 + lane], &cl.bar[par], to, as4(all));
             cl.wait(step);
+#pragma unroll 4
             for (int i = 0; i < rank; ++i) h = apply<R>(load_map(&maps_of[((par) * cs + i) * 32 + lane]), h);
             carry = h;
+#pragma unroll 4
             for (int i = rank; i < cs; ++i) carry = apply<R>(load_map(&maps_of[((par) * cs + i) * 32 + lane]), carry);
         }
         if (p.marks && u == 0 && left > 0)
@@ -334,11 +341,16 @@ scan_bwd_tile_kernel(const __grid_constant__ BwdMaps maps, ScanBwdParams p) {
             if (turn > 0) load(turn - 1 + S);
         // y's map behind this run, and the tile's
         Map behind = unit(), all = load_map(&agg[par][(kWarps - 1) * 32 + lane]);
+        if (u < kWarps - 1) {  // the branches are the warp's
+            behind = all;
 #pragma unroll
-        for (int i = kWarps - 2; i >= 0; --i) {
-            if (i == u) behind = all;
-            all = join<R>(load_map(&agg[par][i * 32 + lane]), all);
+            for (int i = kWarps - 2; i > 0; --i)
+                if (i > u) behind = join<R>(load_map(&agg[par][i * 32 + lane]), behind);
+            all = join<R>({pa, yl}, behind);
         }
+#pragma unroll
+        for (int i = kWarps - 2; i >= 0; --i)
+            if (i < u) all = join<R>(load_map(&agg[par][i * 32 + lane]), all);
         float2 y = carry;
         if (cs == 1) carry = apply<R>(all, y);
         else
@@ -360,8 +372,10 @@ scan_bwd_tile_kernel(const __grid_constant__ BwdMaps maps, ScanBwdParams p) {
         }
         if (cs > 1) {
             cl.wait(turn);
+#pragma unroll 4
             for (int i = cs - 1; i > rank; --i) y = apply<R>(load_map(&maps_of[((par) * cs + i) * 32 + lane]), y);
             carry = y;
+#pragma unroll 4
             for (int i = rank; i >= 0; --i) carry = apply<R>(load_map(&maps_of[((par) * cs + i) * 32 + lane]), carry);
         }
         y = apply<R>(behind, y);
