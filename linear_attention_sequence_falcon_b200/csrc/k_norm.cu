@@ -266,7 +266,7 @@ __device__ __forceinline__ unsigned divide(unsigned n, const FastDiv &f) {
 
 // The offsets of a row's first channel in an array of strided rows (b*sb +
 // h*sh + l*sl), in one of tokens (ld apart) and in one of tokens without gaps.
-// Where all fit 31 bits (p.small), 32-bit arithmetic: a third of the instructions.
+// Where all fit 31 bits (p.small), in 32-bit arithmetic.
 struct GateOffsets {
     long long strided, tokens, packed;
 };
