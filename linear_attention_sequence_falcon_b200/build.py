@@ -1,4 +1,6 @@
-"""Builds libfalcon.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Builds libfalcon.so (the C-ABI library) in-tree with nvcc for sm_100a, and
+_quick.so (csrc/quick_layer.cpp, the short way into the layer operators) with
+g++ against the torch that is installed.
 
     python -m linear_attention_sequence_falcon_b200.build [--force]
 
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfalcon.so")
+QUICK = os.path.join(PKG, "_quick.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -43,6 +46,46 @@ def _stale(target, deps):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    lib = build_library(force, verbose)
+    build_quick(force, verbose)
+    return lib
+
+
+def build_quick(force: bool = False, verbose: bool = False) -> str:
+    """_quick.so: rebuilt when its source, the ABI's header or torch changed."""
+    import sysconfig
+    import torch
+    src = os.path.join(CSRC, "quick_layer.cpp")
+    manifest = os.path.join(BUILD, "quick.txt")
+    made_for = "torch %s, python %s" % (torch.__version__, sys.version)
+    try:
+        same = open(manifest).read() == made_for
+    except OSError:
+        same = not os.path.isdir(BUILD)  # a copy of the tree without its _build/: the module was built elsewhere
+    if not force and same and not _stale(QUICK, [src, os.path.join(INCLUDE, "falcon.h"), os.path.abspath(__file__)]):
+        return QUICK
+    os.makedirs(BUILD, exist_ok=True)
+    base = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_path("include"), os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    tmp = QUICK + ".tmp%d" % os.getpid()
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wno-attributes",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)] + ["-I" + p for p in inc] +
+           [src, "-o", tmp, "-L" + PKG, "-l:libfalcon.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(base, "lib"),
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed: " + " ".join(cmd))
+    os.replace(tmp, QUICK)
+    with open(manifest, "w") as fh:
+        fh.write(made_for)
+    return QUICK
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     deps = _deps()
     # the library is also stale when the set of sources changed (one removed)
     manifest = os.path.join(BUILD, "sources.txt")

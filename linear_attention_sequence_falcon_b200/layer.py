@@ -12,9 +12,12 @@ that made the inputs on another stream is the caller's to wait for.  Rows are
 read through a row stride where the arguments say "rows": [.., L, D] with a
 contiguous last axis whose tokens lie evenly, such as half of a projection.
 
-The small calls are bound by the host (one kernel of 2-3 us behind each), so
-the checks take the short way: sizes, dtype, device index and contiguity in
-one expression, and the words for a refusal only when there is one.
+The small calls are bound by the host (kernels of 2-3 us), so a call whose
+arrays are as they should be, on the current device, goes the short way through
+_quick (csrc/quick_layer.cpp: the same checks, allocations and call in C++, half
+the time).  It answers None for anything else, and the way below is taken: it
+refuses with words, or handles what the short way does not (another device or
+stream, arrays to write into for the norms' passes, a workspace given).
 """
 from __future__ import annotations
 
@@ -24,6 +27,11 @@ import functools
 import torch
 
 from ._lib import DTYPES, FalconError, _check, _shape_error, load
+
+try:
+    from . import _quick
+except ImportError:  # not built (build.py), or for another torch: every call goes the long way
+    _quick = None
 
 SCAN_BLOCK = 64      # tokens between two marks of scan
 NORM_MAX_D = 16384   # the longest row of the norms
@@ -94,6 +102,12 @@ def _apart(t, name):
         span = s * n
 
 
+def _int_sizes(*sizes):
+    for n in sizes:
+        if n > 0x7FFFFFFF:
+            _shape_error("a size of %d does not fit the library's int arguments" % n)
+
+
 def _dtype(t, name):
     if t.dtype not in DTYPES:
         raise FalconError("%s must be fp32 or bf16, got %s" % (name, t.dtype))
@@ -142,6 +156,7 @@ def check_scan_shapes(x, f, reset=None, initial_state=None, out=None, final_stat
     dt = x.dtype
     _dtype(x, "x")
     shape = N, L, D = x.shape
+    _int_sizes(N, L, D)
     at = x.get_device()
     ldx = _rows(x, "x", shape, dt, at)
     ldf = _rows(f, "f", shape, dt, at)
@@ -176,6 +191,10 @@ def scan(x, f, reset=None, initial_state=None, out=None, final_state=None, marks
     packed into one sequence).  Returns (out, final_state), and with
     want_marks the marks that scan_bwd continues from: (out, final_state,
     marks)."""
+    if stream is None and _quick is not None:
+        got = _quick.scan(x, f, reset, initial_state, out, final_state, marks, want_state, want_marks)
+        if got is not None:
+            return got if want_marks else got[:2]
     N, L, D, ldx, ldf = check_scan_shapes(x, f, reset, initial_state, out, final_state, marks)
     at = x.get_device()
     if _elsewhere(at, stream):
@@ -206,6 +225,10 @@ def scan_bwd(x, f, dout, dstate=None, reset=None, initial_state=None, marks=None
     reset and initial_state; without them they are formed again first.
     Returns a dict: dx, df [N,L,D] (written into `dx`, `df` where given: rows)
     and dinitial [N,D] fp32."""
+    if stream is None and _quick is not None:
+        got = _quick.scan_bwd(x, f, dout, dstate, reset, initial_state, marks, dx, df, workspace)
+        if got is not None:
+            return {"dx": got[0], "df": got[1], "dinitial": got[2]}
     N, L, D, ldx, ldf = check_scan_shapes(x, f, reset, initial_state, None, None, marks, dout, dstate)
     at = x.get_device()
     lddx = D if dx is None else _rows(dx, "dx", x.shape, x.dtype, at)
@@ -231,10 +254,15 @@ def scan_step(x, f, state, state_out=None, out=None, stream=None):
     """falcon_scan_step: one token of N sequences, x and f [N,D] (rows), state
     [N,D] fp32.  The new state is written to state_out, or over `state`
     without one.  Returns (out [N,D], the new state)."""
+    if stream is None and _quick is not None:
+        got = _quick.scan_step(x, f, state, state_out, out)
+        if got is not None:
+            return got
     if x.dim() != 2:
         _shape_error("x must be [N,D], got %s" % (tuple(x.shape),))
     dt = _dtype(x, "x")
     shape = N, D = x.shape
+    _int_sizes(N, D)
     at = x.get_device()
     ldx = _rows(x, "x", shape, x.dtype, at)
     ldf = _rows(f, "f", shape, x.dtype, at)
@@ -266,6 +294,7 @@ def check_norm_gate_shapes(o, gate, weight, out=None, dout=None, do=None, dgate=
         _shape_error("o must be [B,H,L,d], got %s" % (tuple(o.shape),))
     _dtype(o, "o")
     B, H, L, d = o.shape
+    _int_sizes(B, H, L)
     if not 1 <= d <= NORM_MAX_D:
         _shape_error("the rows must have 1 to %d channels, got %d" % (NORM_MAX_D, d))
     dt, at, shape = o.dtype, o.get_device(), (B, L, H * d)
@@ -296,6 +325,10 @@ def norm_gate(o, gate, weight, eps: float, out=None, stream=None):
     divided by each row's root mean square, times weight ([d], or [H,d] for
     one per head; None: ones) and z/(1+exp(-z)) of gate [B,L,H*d] (rows; None:
     no gate).  Returns [B,L,H*d], the layout of the output projection."""
+    if stream is None and _quick is not None:
+        got = _quick.norm_gate(o, gate, weight, eps, out)
+        if got is not None:
+            return got
     B, H, L, d, ldg = check_norm_gate_shapes(o, gate, weight, out)
     eps = _eps(eps)
     at = o.get_device()
@@ -326,6 +359,10 @@ def norm_gate_bwd(o, gate, weight, eps: float, dout, do=None, dgate=None, want_d
     dout, or written into `do` with its strides), dgate [B,L,H*d] (rows where
     given; None without a gate), dweight fp32 like weight (None without one,
     or with want_dweight=False)."""
+    if stream is None and do is None and dgate is None and workspace is None and _quick is not None:
+        got = _quick.norm_gate_bwd(o, gate, weight, eps, dout, want_dweight)
+        if got is not None:
+            return {"do": got[0], "dgate": got[1], "dweight": got[2]}
     B, H, L, d, ldg = check_norm_gate_shapes(o, gate, weight, None, dout, do)
     at = o.get_device()
     lddg = H * d
@@ -377,6 +414,7 @@ def check_residual_norm_shapes(r, weight, y=None, scale=None, **like_r):
         _need(scale, "scale", (D,), _F32, at)
     if weight is not None:
         _need(weight, "weight", (D,), _F32, at)
+    _int_sizes(r.numel() // D)
     return r.numel() // D, D
 
 
@@ -385,6 +423,10 @@ def residual_norm(r, weight, eps: float, y=None, scale=None, r_out=None, h=None,
     y, and that divided by its root mean square, times weight [D].  Returns
     (r_out, h); r_out may be `r` itself (the stream updated in place), and is
     `r` where there is no y."""
+    if stream is None and r_out is None and h is None and _quick is not None:
+        got = _quick.residual_norm(r, weight, eps, y, scale)
+        if got is not None:
+            return got
     R, D = check_residual_norm_shapes(r, weight, y, scale, r_out=r_out, h=h)
     eps = _eps(eps)
     if h is not None and r_out is not None and h.data_ptr() == r_out.data_ptr() and R:
@@ -418,6 +460,10 @@ def residual_norm_bwd(r_out, weight, eps: float, dh, dr_out=None, y=None, scale=
     reads the stream; None: zero).  Returns a dict: dr (of r), dy (of y; the
     same tensor as dr without a scale; None without y), dscale, dweight fp32
     (None without scale, weight).  dr may be dr_out or dh."""
+    if stream is None and dr is None and dy is None and workspace is None and _quick is not None:
+        got = _quick.residual_norm_bwd(r_out, weight, eps, dh, dr_out, y, scale)
+        if got is not None:
+            return {"dr": got[0], "dy": got[1], "dscale": got[2], "dweight": got[3]}
     R, D = check_residual_norm_shapes(r_out, weight, y, scale, dh=dh, dr_out=dr_out, dr=dr, dy=dy)
     eps = _eps(eps)
     if dy is not None and scale is None:

@@ -523,6 +523,30 @@ def test_two_graphs_share_nothing(F):
             assert all(torch.equal(p, q) for p, q in zip(layer_calls(F, a), got)), turn
 
 
+def test_short_and_long_way_agree(F, monkeypatch):
+    """layer.py's short way and the way through ctypes: the same kernels, the
+    same bits, the same refusals."""
+    from linear_attention_sequence_falcon_b200 import layer
+    assert layer._quick is not None
+    for a in (layer_args(2, 260, 64, torch.bfloat16, 67), layer_args(1, 130, 34, torch.float32, 71)):
+        short = layer_calls(F, a)
+        monkeypatch.setattr(layer, "_quick", None)
+        long = layer_calls(F, a)
+        monkeypatch.undo()
+        assert len(short) == len(long) and all(torch.equal(p, q) for p, q in zip(short, long))
+        assert all(p.shape == q.shape and p.dtype == q.dtype and p.is_contiguous() == q.is_contiguous() for p, q in zip(short, long))
+    x, f = a["x"], a["f"]
+    assert F.scan(x, f, want_state=0)[1] is None and len(F.scan(x, f, want_marks=1)) == 3
+    with pytest.raises(F.FalconError):
+        F.scan(x, f.bfloat16())
+    with pytest.raises(F.FalconError):
+        F.scan(x, f, initial_state=a["h0"].cpu())
+    with pytest.raises(F.FalconError):
+        F.norm_gate(x[None], None, None, -1.0)
+    with pytest.raises(F.FalconError):
+        F.residual_norm(x.transpose(0, 1), None, 1e-6) if x.shape[0] > 1 else F.residual_norm(x[..., ::2], None, 1e-6)
+
+
 FIRST_CALL = """
 import torch
 import linear_attention_sequence_falcon_b200 as F

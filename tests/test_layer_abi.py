@@ -105,6 +105,27 @@ def test_residual_norm_codes(lib):
         assert bwd(ws=None) == WORKSPACE and bwd(ws_bytes=need - 1) == WORKSPACE and bwd(ws=0x10080) == WORKSPACE
 
 
+def test_short_way_is_built_and_hands_over(lib):
+    """The module behind layer.py's short way is there, and answers None to what
+    it does not take (here: tensors that are not on a GPU, and no tensors)."""
+    from linear_attention_sequence_falcon_b200 import layer
+    q = layer._quick
+    assert q is not None
+    x, s, w = torch.zeros(2, 5, 8), torch.zeros(2, 8), torch.zeros(8)
+    o, r = torch.zeros(2, 3, 5, 8), torch.zeros(4, 8)
+    for t in (x, None, 3):
+        assert q.scan(t, x, None, None, None, None, None, True, False) is None
+        assert q.scan_bwd(t, x, x, None, None, None, None, None, None, None) is None
+        assert q.scan_step(t, s, s, None, None) is None
+        assert q.norm_gate(t, None, w, 1e-6, None) is None
+        assert q.norm_gate_bwd(t, None, w, 1e-6, x, True) is None
+        assert q.residual_norm(t, w, 1e-6, None, None) is None
+        assert q.residual_norm_bwd(t, w, 1e-6, r, None, None, None) is None
+    assert q.norm_gate(o, None, w, "eps", None) is None
+    with pytest.raises(TypeError):
+        q.scan(x)
+
+
 # ---------------------------------------------------------------- the binding (CPU tensors: refused before any pointer)
 
 def _t(*shape, dtype=torch.bfloat16):
