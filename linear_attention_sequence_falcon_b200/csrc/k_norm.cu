@@ -9,7 +9,8 @@
 // data, each array moved once.
 //
 // A row is held by `tpr` threads, VEC neighbouring channels in NC places each
-// (16-byte accesses where the arrays allow, single elements otherwise), so a
+// (16-byte accesses where the arrays allow, two bf16 or single elements
+// otherwise), so a
 // thread keeps its channels from row to row: the weights stay in registers
 // and their gradients are added up there, over the rows that the thread
 // meets, then over the block's rows through shared memory, then over the
@@ -19,6 +20,7 @@
 // two rows' pieces on their way as asynchronous copies into its own places
 // of shared memory (no other thread reads them, so no barrier is needed, and
 // no registers are held).
+#include <algorithm>
 #include <atomic>
 #include <initializer_list>
 #include <type_traits>
@@ -95,7 +97,15 @@ __device__ __forceinline__ void narrow(Piece<float, 1> &p, const float *f) { p.v
 // loaded into registers: bf16 has no asynchronous copy of two bytes, and in fp32
 // copies of four took longer (16 against 14 us backward at 1003x1111).  The
 // widest fp32 rows have no room at all (S = 0) and are read when used.
-template <typename T, int VEC, int NC, int A, int MT, int BLOCKS> struct Ahead {
+//
+// SHIFT: pieces of 16 bytes although rows do not start on them.  Where a row
+// starts within its first piece repeats after VEC rows at most, so a thread that
+// walks rows in steps of such a number finds it the same in each: `lead`
+// elements of the row before, which are read and put to 0, and its channels stay
+// its own.  (All arrays have the same rows here, and start on 16 bytes.)  The
+// residual norm's backward pass of 16384 rows in bf16, against pieces of one
+// element: 74 against 129 us of 1111 channels, 271 against 2303 us of 5001.
+template <typename T, int VEC, int NC, int A, int MT, int BLOCKS, bool SHIFT = false> struct Ahead {
     using P = Piece<T, VEC>;
     static constexpr int kRow = A * NC * (int)sizeof(P);  // bytes per thread
     // rows that fit BLOCKS blocks of an SM; two if one block can have them
@@ -106,12 +116,17 @@ template <typename T, int VEC, int NC, int A, int MT, int BLOCKS> struct Ahead {
     static constexpr int kAhead = S > 0 ? S - 1 : kHeld ? 1 : 0;
     static constexpr int kBytes = S * kRow;
     P *mine;
-    int t, tpr, d, threads;
+    int t, tpr, d, threads, lead;
     const T *at[S == 0 && !kHeld ? A : 1];    // S = 0: the present row
     P held[kHeld ? A : 1][NC], next_[kHeld ? A : 1][NC];
 
-    __device__ __forceinline__ Ahead(uint8_t *smem, int t_, int tpr_, int d_)
-        : mine(reinterpret_cast<P *>(smem) + threadIdx.x), t(t_), tpr(tpr_), d(d_), threads(blockDim.x) {}
+    __device__ __forceinline__ Ahead(uint8_t *smem, int t_, int tpr_, int d_, int lead_ = 0)
+        : mine(reinterpret_cast<P *>(smem) + threadIdx.x), t(t_), tpr(tpr_), d(d_), threads(blockDim.x),
+          lead(SHIFT ? lead_ : 0) {
+        static_assert(!SHIFT || (S > 0 && sizeof(P) == 16), "shifted rows pass through shared memory");
+    }
+    // the first channel of place j (before the row, where a shifted one begins)
+    __device__ __forceinline__ int channel(int j) const { return (j * tpr + t) * VEC - (SHIFT ? lead : 0); }
     __device__ __forceinline__ P *place(int stage, int a, int j) const {
         return mine + ((stage * A + a) * NC + j) * threads;
     }
@@ -130,11 +145,12 @@ template <typename T, int VEC, int NC, int A, int MT, int BLOCKS> struct Ahead {
         } else {
 #pragma unroll
             for (int j = 0; j < NC; ++j) {
-                const int c = (j * tpr + t) * VEC;
+                const int c = channel(j);
                 const bool in = ok && c < d;
                 const uint32_t dst = (uint32_t)__cvta_generic_to_shared(place(stage, a, j));
-                const T *src = in ? row + c : row;
-                const int bytes = in ? (int)sizeof(P) : 0;
+                const T *src = in ? row + c : SHIFT && ok ? row - lead : row;
+                // (a piece that ends behind its row is read up to there, and filled with zeros)
+                const int bytes = !in ? 0 : SHIFT ? min(VEC, d - c) * (int)sizeof(T) : (int)sizeof(P);
                 if constexpr (sizeof(P) == 16)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
                 else
@@ -164,16 +180,29 @@ template <typename T, int VEC, int NC, int A, int MT, int BLOCKS> struct Ahead {
                 widen(v, f + j * VEC);
             } else {
                 widen(*place(stage, a, j), f + j * VEC);
+                if constexpr (SHIFT)
+                    if (j == 0)
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) f[i] = channel(0) + i < 0 ? 0.f : f[i];
             }
         }
     }
     __device__ __forceinline__ void store(T *row, const float *f) const {
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            const int c = (j * tpr + t) * VEC;
+            const int c = channel(j);
             P q;
             narrow(q, f + j * VEC);
-            if (c < d) *reinterpret_cast<P *>(row + c) = q;
+            if (SHIFT && (c < 0 || c + VEC > d)) {  // the row's ends: element by element
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    Piece<T, 1> one;
+                    narrow(one, f + j * VEC + i);
+                    if (c + i >= 0 && c + i < d) *reinterpret_cast<Piece<T, 1> *>(row + c + i) = one;
+                }
+            } else if (c < d) {
+                *reinterpret_cast<P *>(row + c) = q;
+            }
         }
     }
     // the stage behind the present one's last copy, and the next present one
@@ -181,15 +210,15 @@ template <typename T, int VEC, int NC, int A, int MT, int BLOCKS> struct Ahead {
     static __device__ __forceinline__ int next(int stage) { return S <= 1 || stage == S - 1 ? 0 : stage + 1; }
 };
 
-// a thread's channels of an fp32 vector (NULL: ones); 0 behind the row's end
+// a thread's channels of an fp32 vector (NULL: ones); 0 outside of the row
 template <int VEC, int NC>
-__device__ __forceinline__ void load_weights(float *w, const float *p, int t, int tpr, int d) {
+__device__ __forceinline__ void load_weights(float *w, const float *p, int t, int tpr, int d, int lead = 0) {
 #pragma unroll
     for (int j = 0; j < NC; ++j)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const int c = (j * tpr + t) * VEC + i;
-            w[j * VEC + i] = c < d ? (p ? p[c] : 1.f) : 0.f;
+            const int c = (j * tpr + t) * VEC - lead + i;
+            w[j * VEC + i] = c >= 0 && c < d ? (p ? p[c] : 1.f) : 0.f;
         }
 }
 
@@ -247,6 +276,27 @@ __device__ __forceinline__ void block_part(float *acc, int t, int tpr, int slot,
             const int c = (j * tpr + t) * VEC + i;
             if (c < d) part[c] = acc[j * VEC + i];
         }
+}
+
+// the same where each slot's rows have a lead of their own, so that a thread's
+// channels are not those of its place in another slot: joined by channel
+template <int VEC, int NC>
+__device__ __forceinline__ void block_part_shifted(const float *acc, int t, int tpr, int lead, int slot, int slots, int d,
+                                                   float *part, float *buf) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int c = (j * tpr + t) * VEC - lead + i;
+            if (c >= 0 && c < d) buf[slot * d + c] = acc[j * VEC + i];
+        }
+    __syncthreads();
+    for (int c = threadIdx.x; c < d; c += blockDim.x) {
+        float sum = buf[c];
+        for (int i = 1; i < slots; ++i) sum += buf[i * d + c];
+        part[c] = sum;
+    }
 }
 
 // ---- the rows of the gated norm: (b, l, h) with h innermost, or, where a
@@ -413,16 +463,16 @@ __global__ void __launch_bounds__(MT, bwd_blocks(MT, VEC, VEC * NC)) norm_gate_b
                             reinterpret_cast<float *>(smem));
 }
 
-template <typename T, int VEC, int NC, int MT, bool ADD>
+template <typename T, int VEC, int NC, int MT, bool ADD, bool SHIFT>
 __global__ void __launch_bounds__(MT, fwd_blocks(MT, VEC * NC)) residual_norm_kernel(ResidualNormParams p, int tpr) {
     constexpr int E = VEC * NC;
-    using Rows = Ahead<T, VEC, NC, ADD ? 2 : 1, MT, fwd_blocks(MT, VEC * NC)>;
+    using Rows = Ahead<T, VEC, NC, ADD ? 2 : 1, MT, fwd_blocks(MT, VEC * NC), SHIFT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][32][2];
     const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, d = p.D;
-    Rows rows(smem, t, tpr, d);
     const long long step = (long long)gridDim.x * slots;
     long long row = (long long)blockIdx.x * slots + slot, ahead = row;
+    Rows rows(smem, t, tpr, d, (int)((unsigned)row * (unsigned)d) & (VEC - 1));
     auto fetch = [&](int stage) {
         const bool ok = ahead < p.R;
         const long long at = ok ? ahead * d : 0;
@@ -433,8 +483,8 @@ __global__ void __launch_bounds__(MT, fwd_blocks(MT, VEC * NC)) residual_norm_ke
     };
     for (int i = 0; i < Rows::kAhead; ++i) fetch(i);
     float wt[E], sc[E];
-    load_weights<VEC, NC>(wt, p.weight, t, tpr, d);
-    if constexpr (ADD) load_weights<VEC, NC>(sc, p.scale, t, tpr, d);
+    load_weights<VEC, NC>(wt, p.weight, t, tpr, d, rows.lead);
+    if constexpr (ADD) load_weights<VEC, NC>(sc, p.scale, t, tpr, d, rows.lead);
     int parity = 0, stage = 0;
     for (long long base = (long long)blockIdx.x * slots; base < p.R; base += step, parity ^= 1) {
         fetch(Rows::last(stage));
@@ -461,16 +511,16 @@ __global__ void __launch_bounds__(MT, fwd_blocks(MT, VEC * NC)) residual_norm_ke
     }
 }
 
-template <typename T, int VEC, int NC, int MT, bool ADD>
+template <typename T, int VEC, int NC, int MT, bool ADD, bool SHIFT>
 __global__ void __launch_bounds__(MT, bwd_blocks(MT, VEC, VEC * NC)) residual_norm_bwd_kernel(ResidualNormParams p, int tpr) {
     constexpr int E = VEC * NC;
-    using Rows = Ahead<T, VEC, NC, ADD ? 4 : 3, MT, bwd_blocks(MT, VEC, VEC * NC)>;
+    using Rows = Ahead<T, VEC, NC, ADD ? 4 : 3, MT, bwd_blocks(MT, VEC, VEC * NC), SHIFT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][32][2];
     const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, d = p.D;
-    Rows rows(smem, t, tpr, d);
     const long long step = (long long)gridDim.x * slots;
     long long row = (long long)blockIdx.x * slots + slot, ahead = row;
+    Rows rows(smem, t, tpr, d, (int)((unsigned)row * (unsigned)d) & (VEC - 1));
     const bool stream = p.dr_out != nullptr;
     auto fetch = [&](int stage) {
         const bool ok = ahead < p.R;
@@ -484,8 +534,8 @@ __global__ void __launch_bounds__(MT, bwd_blocks(MT, VEC, VEC * NC)) residual_no
     };
     for (int i = 0; i < Rows::kAhead; ++i) fetch(i);
     float wt[E], sc[E], dw[E], ds[E];
-    load_weights<VEC, NC>(wt, p.weight, t, tpr, d);
-    load_weights<VEC, NC>(sc, p.scale, t, tpr, d);
+    load_weights<VEC, NC>(wt, p.weight, t, tpr, d, rows.lead);
+    load_weights<VEC, NC>(sc, p.scale, t, tpr, d, rows.lead);
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[e] = ds[e] = 0.f;
     const float inv_d = 1.f / d;
@@ -533,10 +583,15 @@ __global__ void __launch_bounds__(MT, bwd_blocks(MT, VEC, VEC * NC)) residual_no
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Rows::wait_all();
     float *buf = reinterpret_cast<float *>(smem);
-    if (p.dweight) block_part<VEC, NC>(dw, t, tpr, slot, slots, d, p.ws + (long long)blockIdx.x * d, buf);
+    auto join = [&](float *acc, long long at) {
+        if constexpr (SHIFT)
+            block_part_shifted<VEC, NC>(acc, t, tpr, rows.lead, slot, slots, d, p.ws + at * d, buf);
+        else
+            block_part<VEC, NC>(acc, t, tpr, slot, slots, d, p.ws + at * d, buf);
+    };
+    if (p.dweight) join(dw, blockIdx.x);
     if constexpr (ADD)
-        if (p.dscale)
-            block_part<VEC, NC>(ds, t, tpr, slot, slots, d, p.ws + ((long long)gridDim.x + blockIdx.x) * d, buf);
+        if (p.dscale) join(ds, (long long)gridDim.x + blockIdx.x);
 }
 
 // out[c] = sum over i of part[i*n + c]: 32 channels per block, kSegments runs
@@ -698,6 +753,36 @@ NormGateParams divided(NormGateParams p) {
     return p;
 }
 
+// the rows of the residual norm: their layout, and whether they are shifted (a
+// layout then has room for the lead, and blocks walk rows in steps after which
+// the lead repeats)
+constexpr int kShiftThreads = 512;
+struct ResidualRows {
+    int d, vec;
+    bool shift;
+    Layout lay;
+    ResidualRows(int d_, Kind kind, int vec_, bool shift_)
+        : d(d_), vec(vec_), shift(shift_), lay(shift_ ? d_ + vec_ - 1 : d_, kind, vec_) {}
+    int whole(int blocks, int most) const {
+        int q = 1;
+        while (shift && (long long)q * lay.slots * d % vec) q *= 2;
+        const int up = (blocks + q - 1) / q * q;
+        return up <= most ? up : most / q * q;
+    }
+    int forward_blocks(long long rows) const { return whole(lay.forward_blocks(rows), lay.forward_blocks(1ll << 60)); }
+    int backward_blocks(long long rows) const {
+        return whole(lay.backward_blocks(rows, rows), lay.backward_blocks(1ll << 60, 1ll << 60));
+    }
+};
+template <typename T> ResidualRows residual_rows(int d, Kind kind, std::initializer_list<const void *> arrays) {
+    constexpr int wide = 16 / (int)sizeof(T);
+    const int vec = pieces<T>(arrays, {d});
+    bool shift = vec < wide;
+    for (const void *p : arrays) shift = shift && vec_ok(p);
+    const ResidualRows shifted(d, kind, wide, true);
+    return shift && shifted.lay.threads <= kShiftThreads ? shifted : ResidualRows(d, kind, vec, false);
+}
+
 }  // namespace
 
 size_t norm_gate_bwd_ws_bytes(int, int B, int H, int L, int d) {
@@ -713,7 +798,11 @@ size_t norm_gate_bwd_ws_bytes(int, int B, int H, int L, int d) {
     return sizeof(float) * most;
 }
 size_t residual_norm_bwd_ws_bytes(int, int R, int D) {
-    return sizeof(float) * 2 * (size_t)Layout(D, kResidualBackward).backward_blocks(R, R) * D;
+    // for any type and alignment
+    const int plain = Layout(D, kResidualBackward).backward_blocks(R, R);
+    const int four = ResidualRows(D, kResidualBackward, 4, true).backward_blocks(R),
+              eight = ResidualRows(D, kResidualBackward, 8, true).backward_blocks(R);
+    return sizeof(float) * 2 * (size_t)std::max(plain, std::max(four, eight)) * D;
 }
 
 template <typename T> int launch_norm_gate(const NormGateParams &q, cudaStream_t s) {
@@ -747,24 +836,34 @@ template <typename T> int launch_norm_gate_bwd(const NormGateParams &q, cudaStre
 }
 
 template <typename T> int launch_residual_norm(const ResidualNormParams &p, cudaStream_t s) {
-    const int vec = pieces<T>({p.r, p.y, p.r_out, p.h}, {p.D});
-    const Layout lay(p.D, kForward, vec);
-    const unsigned grid = (unsigned)lay.forward_blocks(p.R);
-    return with_layout<T, true>(lay, vec, [&](auto v, auto nc, auto mt) {
+    const auto rows = residual_rows<T>(p.D, kForward, {p.r, p.y, p.r_out, p.h});
+    const unsigned grid = (unsigned)rows.forward_blocks(p.R);
+    return with_layout<T, true>(rows.lay, rows.vec, [&](auto v, auto nc, auto mt) {
         constexpr int V = v(), N = nc(), M = mt(), B = fwd_blocks(M, V * N);
-        return p.y ? launch<residual_norm_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 2, M, B>(lay.threads), ring_bytes<T, V, N, 2, M, B>(M), s, p, lay.tpr)
-                   : launch<residual_norm_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 1, M, B>(lay.threads), ring_bytes<T, V, N, 1, M, B>(M), s, p, lay.tpr);
+        auto go = [&](auto add, auto shift) {
+            constexpr int A = add() ? 2 : 1;
+            return launch<residual_norm_kernel<T, V, N, M, add(), shift()>>(
+                grid, rows.lay.threads, ring_bytes<T, V, N, A, M, B>(rows.lay.threads), ring_bytes<T, V, N, A, M, B>(M), s, p, rows.lay.tpr);
+        };
+        if constexpr (V == 16 / (int)sizeof(T) && M <= kShiftThreads)
+            if (rows.shift) return p.y ? go(std::true_type(), std::true_type()) : go(std::false_type(), std::true_type());
+        return p.y ? go(std::true_type(), std::false_type()) : go(std::false_type(), std::false_type());
     });
 }
 
 template <typename T> int launch_residual_norm_bwd(const ResidualNormParams &p, cudaStream_t s) {
-    const Layout lay(p.D, kResidualBackward);
-    const int vec = pieces<T>({p.r, p.y, p.dh, p.dr_out, p.dr, p.dy}, {p.D});
-    const unsigned grid = (unsigned)lay.backward_blocks(p.R, p.R);
-    with_layout<T, false>(lay, vec, [&](auto v, auto nc, auto mt) {
+    const auto rows = residual_rows<T>(p.D, kResidualBackward, {p.r, p.y, p.dh, p.dr_out, p.dr, p.dy});
+    const unsigned grid = (unsigned)rows.backward_blocks(p.R);
+    with_layout<T, false>(rows.lay, rows.vec, [&](auto v, auto nc, auto mt) {
         constexpr int V = v(), N = nc(), M = mt(), B = bwd_blocks(M, V, V * N);
-        return p.y ? launch<residual_norm_bwd_kernel<T, V, N, M, true>>(grid, lay.threads, ring_bytes<T, V, N, 4, M, B>(lay.threads), ring_bytes<T, V, N, 4, M, B>(M), s, p, lay.tpr)
-                   : launch<residual_norm_bwd_kernel<T, V, N, M, false>>(grid, lay.threads, ring_bytes<T, V, N, 3, M, B>(lay.threads), ring_bytes<T, V, N, 3, M, B>(M), s, p, lay.tpr);
+        auto go = [&](auto add, auto shift) {
+            constexpr int A = add() ? 4 : 3;
+            return launch<residual_norm_bwd_kernel<T, V, N, M, add(), shift()>>(
+                grid, rows.lay.threads, ring_bytes<T, V, N, A, M, B>(rows.lay.threads), ring_bytes<T, V, N, A, M, B>(M), s, p, rows.lay.tpr);
+        };
+        if constexpr (V == 16 / (int)sizeof(T) && M <= kShiftThreads)
+            if (rows.shift) return p.y ? go(std::true_type(), std::true_type()) : go(std::false_type(), std::true_type());
+        return p.y ? go(std::true_type(), std::false_type()) : go(std::false_type(), std::false_type());
     });
     if (p.dweight || p.dscale) return launch_sums(p.ws, (int)grid, p.D, p.dweight, p.dscale, s);
     return 0;

@@ -408,6 +408,49 @@ def test_residual_norm_in_place_and_borders(F, R, D, offset, dtype):
     same(F.residual_norm_bwd(rr, w, 1e-6, dd, dr_out=dr, y=yy, scale=s, dr=dd))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("R,D", [(5003, 281), (2999, 1111), (700, 2047), (301, 4097), (40, 8185), (40, 8187), (2501, 33), (4001, 12), (9000, 1), (1501, 1110), (3, 7)])
+def test_residual_norm_rows_off_the_pieces(F, R, D, dtype):
+    """Rows that do not start on 16 bytes, in arrays that do: many rows to a
+    thread, neighbours of NaN and infinities, the ends of each row, in place."""
+    t = TYPES[dtype]
+    g = gen(R * 3 + D)
+    r, y, dh, dr = (normal(g, R, D, dtype=t) for _ in range(4))
+    s, w = normal(g, D), normal(g, D)
+    (ws, bs), (wh, bh) = ref.residual_norm(np64(r), np64(y), np64(s), np64(w), 1e-6)
+    rr, rb, st, n = guarded((R, D), t, 0)
+    yy, yb, _, _ = guarded((R, D), t, 0)
+    assert rr.data_ptr() % 16 == 0 and yy.data_ptr() % 16 == 0
+    rr.copy_(r)
+    yy.copy_(y)
+    F.residual_norm(rr, w, 1e-6, y=yy, scale=s, r_out=rr, h=yy)
+    untouched(rb, st, n)
+    untouched(yb, st, n)
+    ref.check(rr, ws, bs, t, "r_out")
+    ref.check(yy, wh, bh, t, "h")
+    got = F.residual_norm_bwd(rr, w, 1e-6, dh, dr_out=dr, y=y, scale=s)
+    want = ref.residual_norm_bwd(np64(rr), np64(y), np64(s), np64(w), 1e-6, np64(dh), np64(dr))
+    for k in want:
+        ref.check(got[k], *want[k], t if k in ("dr", "dy") else torch.float32, k)
+    dd, db, _, _ = guarded((R, D), t, 0)
+    dd.copy_(dr)
+    again = F.residual_norm_bwd(rr, w, 1e-6, dh, dr_out=dd, y=y, scale=s, dr=dd)
+    untouched(db, st, n)
+    assert all(torch.equal(got[k], again[k]) for k in got)
+    # a row's outputs are its own: bad numbers in every third row stay there
+    bad = dh.clone()
+    bad[::3] = float("nan")
+    bad[1::6] = float("inf")
+    kept = [i for i in range(R) if i % 3 and i % 6 != 1]
+    if kept:
+        ill = F.residual_norm_bwd(rr, w, 1e-6, bad, dr_out=dr, y=y, scale=s)
+        assert torch.equal(ill["dr"][kept], got["dr"][kept]) and torch.equal(ill["dy"][kept], got["dy"][kept])
+        worse = r.clone()
+        worse[::3] = float("nan")
+        worse[1::6] = float("inf")
+        assert torch.equal(F.residual_norm(worse, w, 1e-6, y=y, scale=s)[1][kept], yy[kept])
+
+
 def test_norms_gradients_against_differences(F):
     """The kernels' gradients along a direction against central differences of
     the fp64 formulas (a step of 1e-5: 1e-10 of the terms; the fp32 gradients
