@@ -10,11 +10,10 @@
 //
 // A row is held by `tpr` threads, VEC neighbouring channels in NC places each
 // (16-byte accesses where the arrays allow, two bf16 or single elements
-// otherwise), so a
-// thread keeps its channels from row to row: the weights stay in registers
-// and their gradients are added up there, over the rows that the thread
-// meets, then over the block's rows through shared memory, then over the
-// blocks by sum_parts_kernel.  All orders are fixed by the sizes.
+// otherwise), so a thread keeps its channels from row to row: the weights stay
+// in registers and their gradients are added up there, over the rows that the
+// thread meets, then over the block's rows through shared memory, then over
+// the blocks by sum_parts_kernel.  All orders are fixed by the sizes.
 //
 // The bound is HBM: what it takes is bytes in flight.  A thread keeps the next
 // two rows' pieces on their way as asynchronous copies into its own places
@@ -629,12 +628,36 @@ __global__ void __launch_bounds__(32 * kSegments) sum_parts_kernel(const float *
 // a row costs beside its channels, and up to 1024 channels a row stays inside a
 // warp, which needs no barrier, with up to 32 (not in single elements, whose
 // loads are held in registers one by one).
+//
+// A block's warps go round the SM's four schedulers, so five warps take a block
+// as long as eight: what a row costs is the channels that its turns could
+// carry, `carried`.  Beyond 1024 channels a forward row that fills less than
+// four fifths of that takes 24 or 32 channels a thread where they carry less,
+// if there are rows for blocks on every SM (16384 rows of bf16: 28 against 35 us
+// of 1112 channels, 36 against 42 of 1536, 92 against 136 of 4097; of 6000, which
+// fill theirs, 16 channels take 128 and 24 take 146).  fp32, with twice the
+// bytes to a channel, gains up to 2048 only (54 against 60 us of 1111; 202 against
+// 177 of 4097).
 enum Kind { kForward, kGateBackward, kResidualBackward };
 struct Layout {
     int each, tpr, threads, slots;
-    Layout(int d, Kind kind, int vec = 1) {
-        each = d > 2048 || (kind == kGateBackward && vec > 1 && d > 32) ? 16 : 8;
-        if (kind == kForward && vec > 1 && d > 64 && d <= 1024) each = d <= 256 ? 16 : (d + 255) / 256 * 8;
+    Layout(int d, Kind kind, int vec = 1, long long rows = 0) {
+        int channels = d > 2048 || (kind == kGateBackward && vec > 1 && d > 32) ? 16 : 8;
+        if (kind == kForward && vec > 1 && d > 64 && d <= 1024) channels = d <= 256 ? 16 : (d + 255) / 256 * 8;
+        lay(d, channels);
+        if (kind != kForward || vec == 1 || d <= 1024 || d > (vec == 4 ? 2048 : 8192) || d * 5 >= carried() * 4) return;
+        const Layout first = *this;
+        Layout best = first;
+        for (int more = 24; more <= 32; more += 8) {
+            lay(d, more);
+            if (threads <= 256 && rows >= (long long)slots * kSms &&
+                (carried() < best.carried() || (best.each == first.each && carried() == best.carried())))
+                best = *this;
+        }
+        *this = best;
+    }
+    void lay(int d, int channels) {
+        each = channels;
         const int need = (d + each - 1) / each;
         if (need > 32) {
             tpr = (need + 31) / 32 * 32;
@@ -645,6 +668,7 @@ struct Layout {
         slots = tpr >= 256 ? 1 : 256 / tpr;
         threads = tpr * slots;
     }
+    int carried() const { return each * ((threads + 127) / 128 * 128) / slots; }
     // blocks for `rows` rows: `per_sm` (of at most 256 threads) on every SM, at
     // least `least` rows each where there are as many
     int blocks(long long rows, int per_sm, int least) const {
@@ -761,8 +785,8 @@ struct ResidualRows {
     int d, vec;
     bool shift;
     Layout lay;
-    ResidualRows(int d_, Kind kind, int vec_, bool shift_)
-        : d(d_), vec(vec_), shift(shift_), lay(shift_ ? d_ + vec_ - 1 : d_, kind, vec_) {}
+    ResidualRows(int R, int d_, Kind kind, int vec_, bool shift_)
+        : d(d_), vec(vec_), shift(shift_), lay(shift_ ? d_ + vec_ - 1 : d_, kind, vec_, R) {}
     int whole(int blocks, int most) const {
         int q = 1;
         while (shift && (long long)q * lay.slots * d % vec) q *= 2;
@@ -774,13 +798,13 @@ struct ResidualRows {
         return whole(lay.backward_blocks(rows, rows), lay.backward_blocks(1ll << 60, 1ll << 60));
     }
 };
-template <typename T> ResidualRows residual_rows(int d, Kind kind, std::initializer_list<const void *> arrays) {
+template <typename T> ResidualRows residual_rows(int R, int d, Kind kind, std::initializer_list<const void *> arrays) {
     constexpr int wide = 16 / (int)sizeof(T);
     const int vec = pieces<T>(arrays, {d});
     bool shift = vec < wide;
     for (const void *p : arrays) shift = shift && vec_ok(p);
-    const ResidualRows shifted(d, kind, wide, true);
-    return shift && shifted.lay.threads <= kShiftThreads ? shifted : ResidualRows(d, kind, vec, false);
+    const ResidualRows shifted(R, d, kind, wide, true);
+    return shift && shifted.lay.threads <= kShiftThreads ? shifted : ResidualRows(R, d, kind, vec, false);
 }
 
 }  // namespace
@@ -800,15 +824,15 @@ size_t norm_gate_bwd_ws_bytes(int, int B, int H, int L, int d) {
 size_t residual_norm_bwd_ws_bytes(int, int R, int D) {
     // for any type and alignment
     const int plain = Layout(D, kResidualBackward).backward_blocks(R, R);
-    const int four = ResidualRows(D, kResidualBackward, 4, true).backward_blocks(R),
-              eight = ResidualRows(D, kResidualBackward, 8, true).backward_blocks(R);
+    const int four = ResidualRows(R, D, kResidualBackward, 4, true).backward_blocks(R),
+              eight = ResidualRows(R, D, kResidualBackward, 8, true).backward_blocks(R);
     return sizeof(float) * 2 * (size_t)std::max(plain, std::max(four, eight)) * D;
 }
 
 template <typename T> int launch_norm_gate(const NormGateParams &q, cudaStream_t s) {
     const NormGateParams p = divided(q);
     const int vec = pieces<T>({p.o, p.gate, p.out}, {p.d, p.o_sb, p.o_sh, p.o_sl, p.gate ? p.ldg : 0});
-    const Layout lay(p.d, kForward, vec);
+    const Layout lay(p.d, kForward, vec, (long long)p.B * p.L * (p.per_head ? 1 : p.H));
     const int parts = gate_parts(lay, p, true);
     const unsigned grid = (unsigned)parts * (p.per_head ? p.H : 1);
     return with_layout<T, true>(lay, vec, [&](auto v, auto nc, auto mt) {
@@ -836,7 +860,7 @@ template <typename T> int launch_norm_gate_bwd(const NormGateParams &q, cudaStre
 }
 
 template <typename T> int launch_residual_norm(const ResidualNormParams &p, cudaStream_t s) {
-    const auto rows = residual_rows<T>(p.D, kForward, {p.r, p.y, p.r_out, p.h});
+    const auto rows = residual_rows<T>(p.R, p.D, kForward, {p.r, p.y, p.r_out, p.h});
     const unsigned grid = (unsigned)rows.forward_blocks(p.R);
     return with_layout<T, true>(rows.lay, rows.vec, [&](auto v, auto nc, auto mt) {
         constexpr int V = v(), N = nc(), M = mt(), B = fwd_blocks(M, V * N);
@@ -852,7 +876,7 @@ template <typename T> int launch_residual_norm(const ResidualNormParams &p, cuda
 }
 
 template <typename T> int launch_residual_norm_bwd(const ResidualNormParams &p, cudaStream_t s) {
-    const auto rows = residual_rows<T>(p.D, kResidualBackward, {p.r, p.y, p.dh, p.dr_out, p.dr, p.dy});
+    const auto rows = residual_rows<T>(p.R, p.D, kResidualBackward, {p.r, p.y, p.dh, p.dr_out, p.dr, p.dy});
     const unsigned grid = (unsigned)rows.backward_blocks(p.R);
     with_layout<T, false>(rows.lay, rows.vec, [&](auto v, auto nc, auto mt) {
         constexpr int V = v(), N = nc(), M = mt(), B = bwd_blocks(M, V, V * N);
