@@ -94,8 +94,8 @@ __device__ __forceinline__ void narrow(Piece<float, 1> &p, const float *f) { p.v
 // S rows in shared memory (three where they fit the block's, whatever fits
 // otherwise), S - 1 of them on their way.  Of single elements the next row's are
 // loaded into registers: bf16 has no asynchronous copy of two bytes, and in fp32
-// copies of four took longer (16 against 14 us backward at 1003x1111).  The
-// widest fp32 rows have no room at all (S = 0) and are read when used.
+// copies of four took longer (backward at 1003x1111 off 16 bytes, 16 against
+// 14 us).  The widest fp32 rows have no room at all (S = 0) and are read when used.
 //
 // SHIFT: pieces of 16 bytes although rows do not start on them.  Where a row
 // starts within its first piece repeats after VEC rows at most, so a thread that
@@ -103,7 +103,7 @@ __device__ __forceinline__ void narrow(Piece<float, 1> &p, const float *f) { p.v
 // elements of the row before, which are read and put to 0, and its channels stay
 // its own.  (All arrays have the same rows here, and start on 16 bytes.)  The
 // residual norm's backward pass of 16384 rows in bf16, against pieces of one
-// element: 74 against 129 us of 1111 channels, 271 against 2303 us of 5001.
+// element: 62 against 129 us of 1111 channels, 223 against 2303 us of 5001.
 template <typename T, int VEC, int NC, int A, int MT, int BLOCKS, bool SHIFT = false> struct Ahead {
     using P = Piece<T, VEC>;
     static constexpr int kRow = A * NC * (int)sizeof(P);  // bytes per thread
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(32 * kSegments) sum_parts_kernel(const float *
 // as long as eight: what a row costs is the channels that its turns could
 // carry, `carried`.  Beyond 1024 channels a forward row that fills less than
 // four fifths of that takes 24 or 32 channels a thread where they carry less,
-// if there are rows for blocks on every SM (16384 rows of bf16: 28 against 35 us
+// if there are rows for blocks on every SM (16384 rows of bf16: 27 against 35 us
 // of 1112 channels, 36 against 42 of 1536, 92 against 136 of 4097; of 6000, which
 // fill theirs, 16 channels take 128 and 24 take 146).  fp32, with twice the
 // bytes to a channel, gains up to 2048 only (54 against 60 us of 1111; 202 against
