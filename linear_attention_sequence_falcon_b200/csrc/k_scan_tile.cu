@@ -125,10 +125,13 @@ template <typename T, int A, int FEED> struct Ring {
         return FEED != kTensor || tc::mbar_wait_timeout(&full[turn % S], (turn / S) & 1, kGiveUpNs);
     }
     // tokens behind the sequence's end (zeros, as the copies fill them) keep the
-    // state: f (array 1) = +inf, each thread at its own channels
+    // state: f (array 1) = +inf, each thread at its own channels.  Backward they
+    // come first, and a later tile's copy writes the same bytes: the stores are
+    // ordered in front of it by the fence here and the barrier before that copy.
     __device__ __forceinline__ void keep_behind(int turn, int left) const {
         const T inf = from_f32<T>(__int_as_float(0x7f800000));
         for (int i = left < 0 ? 0 : left; i < kRun; ++i) place(turn, 1, i)[0] = place(turn, 1, i)[kGap] = inf;
+        if constexpr (FEED == kTensor) tc::fence_proxy_async();
     }
     // given up: the copies still on their way land before the block's memory goes
     __device__ __forceinline__ void drain() {

@@ -94,6 +94,41 @@ def test_scan_forward_backward(F, N, L, D, reset, initial, dtype):
     assert torch.equal(out, F.scan(x, f, reset=m, initial_state=h0, want_state=False)[0])
 
 
+# Long sequences of few channels: five turns of the cluster's walk at least, so
+# that every place of the tiles' ring and both halves of the cluster's exchange
+# are used again, and a ragged end.  (A tile is 64 tokens beyond 32 channels,
+# and 4096 tokens over the channels rounded up to 8, 16 or 32 below that.)
+STEPS = [
+    (1, 6001, 64), (1, 6001, 66), (1, 6001, 67),                  # bf16: the three ways tiles come; fp32: two
+    (1, 10001, 24), (1, 17001, 16), (1, 33001, 5), (2, 5185, 96),
+    (197, 330, 130),                                              # blocks that need no neighbours: six turns of their own
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("reset", ["none", "random"])
+@pytest.mark.parametrize("N,L,D", STEPS)
+def test_scan_many_steps(F, N, L, D, reset, dtype):
+    t = TYPES[dtype]
+    tile = 64 if D > 32 else 4096 // max(8, 1 << (D - 1).bit_length())
+    assert N > 2 or -(-(-(-L // tile)) // 16) >= 5 and L % tile
+    x, f, m, h0, dout, dstate = scan_case(N, L, D, reset, True, t, N + L + D)
+    out, state, marks = F.scan(x, f, reset=m, initial_state=h0, want_marks=True)
+    args = np64(x), np64(f), None if m is None else m.cpu().numpy(), np64(h0)
+    h, b, _, _ = ref.scan(*args)
+    ref.check(out, h, b, t, "out")
+    ref.check(state, h[:, -1], b[:, -1], torch.float32, "state")
+    blocks = range(F.SCAN_BLOCK, L, F.SCAN_BLOCK)
+    ref.check(marks[:, 1:], h[:, [i - 1 for i in blocks]], b[:, [i - 1 for i in blocks]], torch.float32, "marks")
+    r = ref.scan_bwd(args[0], args[1], np64(dout), np64(dstate), args[2], args[3])
+    first = F.scan_bwd(x, f, dout, dstate=dstate, reset=m, initial_state=h0, marks=marks)
+    for g in (first, F.scan_bwd(x, f, dout, dstate=dstate, reset=m, initial_state=h0)):
+        ref.check(g["dx"], *r["dx"], t, "dx")
+        ref.check(g["df"], *r["df"], t, "df")
+        ref.check(g["dinitial"], *r["dinitial"], torch.float32, "dinitial")
+        assert all(torch.equal(first[k], g[k]) for k in g)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_scan_gradients_against_differences(F, dtype):
     """The kernel's gradient along a direction against a central difference of
