@@ -44,23 +44,28 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 
 // a = sigmoid(f), c = 1 - a.
 //
-// fp32: each to full relative accuracy, without a branch on f's sign: e =
-// exp(-f), a = 1/(1+e), c = e a.  The exponent is held at 115 (f = -79.7: a is
-// 2e-35 from there on), so that e a stays finite; one Newton step takes the
-// reciprocal's last bit, since a gradient through a thousand tokens is a
-// product of as many a's (the initial state's was off by 6e-7 to 9e-7, with the
-// step by 3e-7).
-// bf16: c = 1/(1+exp(f)) to full relative accuracy, a = 1 - c rounded once, so
-// off by 2^-25 at most.  Where a is near 1, and products of it are long, that
-// is its last bit; where it is small it is small beside c x.  A third of the
-// instructions less.
+// Both with relative accuracy, a where it is near 0 too: df and the initial
+// state's gradient are proportional to it, and so is the state where x is 0.
+// In U = 2^-24 of the value: the exponent's argument is rounded once (with
+// log2(e) itself |f| 1.22 U), ex2 is off by 3 U, rcp by 2 U, each sum and
+// product by 1 U.
+//
+// fp32, without a branch on f's sign: e = exp(-f), a = 1/(1+e), c = e a.  The
+// exponent is held at 115 (f = -79.7: a is 2e-35 from there on), so that e a
+// stays finite; one Newton step takes the reciprocal's last bit, since a
+// gradient through a thousand tokens is a product of as many a's (the initial
+// state's was off by 6e-7 to 9e-7, with the step by 3e-7).
+// bf16: e = exp(f), c = 1/(1+e), and a = 1 - c for f >= 0, where it is off by 3
+// U at most and near 1 by its last bit, which counts where products of it are
+// long; e c below 0, (1.22 |f| + 7) U off.  (1 - c alone loses a below f = -11
+// and is 0 from -17 on.)
 template <typename T> __device__ __forceinline__ void gates(float2 f, float2 &a, float2 &c) {
     constexpr float kLog2e = 1.4426950408889634f;
     const float2 one = make_float2(1.f, 1.f);
     if constexpr (sizeof(T) == 2) {
-        const float2 z = mul2(f, make_float2(kLog2e, kLog2e)), s = add2(make_float2(ex2(z.x), ex2(z.y)), one);
+        const float2 z = mul2(f, make_float2(kLog2e, kLog2e)), e = make_float2(ex2(z.x), ex2(z.y)), s = add2(e, one);
         c = make_float2(rcp(s.x), rcp(s.y));
-        a = make_float2(1.f - c.x, 1.f - c.y);
+        a = make_float2(e.x < 1.f ? e.x * c.x : 1.f - c.x, e.y < 1.f ? e.y * c.y : 1.f - c.y);
     } else {
         const float2 z = mul2(f, make_float2(-kLog2e, -kLog2e));
         const float2 e = make_float2(ex2(min_nan(z.x, 115.f)), ex2(min_nan(z.y, 115.f)));

@@ -29,12 +29,12 @@ def sigmoid(z):
     return np.where(z < 0, e / (1 + e), 1 / (1 + e))
 
 
-def scan(x, f, reset=None, initial=None, dtype=torch.float32):
+def scan(x, f, reset=None, initial=None, dtype=torch.float32, far=1.0):
     """h [N,L,D] and its fp32 bound before rounding.  The bound follows the
     recurrence: every step scales what is there by a and adds (|f|+12+4) U of
     the step's two terms in absolute value (their products and sum; the 4
     covers the products of a's formed over runs of tokens, one more rounding
-    for each factor)."""
+    for each factor).  `far`: how many U of itself a gate is off per unit of |f|."""
     N, L, D = x.shape
     a, c = sigmoid(f), sigmoid(-f)
     h = np.zeros((N, L, D))
@@ -47,7 +47,7 @@ def scan(x, f, reset=None, initial=None, dtype=torch.float32):
         r = np.zeros((N, 1), bool) if reset is None else reset[:, t, None].astype(bool)
         s, mag, e = np.where(r, 0, s), np.where(r, 0, mag), np.where(r, 0, e)
         before[:, t], ebefore[:, t] = s, e
-        k = np.minimum(np.abs(f[:, t]), 100) + 16
+        k = far * np.minimum(np.abs(f[:, t]), 100) + 16
         step = a[:, t] * mag + c[:, t] * np.abs(x[:, t])
         e = a[:, t] * e + k * U * step
         mag = step
@@ -56,16 +56,16 @@ def scan(x, f, reset=None, initial=None, dtype=torch.float32):
     return h, bound, before, ebefore
 
 
-def scan_bwd(x, f, dout, dstate=None, reset=None, initial=None):
+def scan_bwd(x, f, dout, dstate=None, reset=None, initial=None, far=1.0):
     """dx, df, dinitial, each with its fp32 bound before rounding."""
     N, L, D = x.shape
-    _, _, before, ebefore = scan(x, f, reset, initial)
+    _, _, before, ebefore = scan(x, f, reset, initial, far=far)
     a, c = sigmoid(f), sigmoid(-f)
     g = np.zeros((N, D)) if dstate is None else dstate.copy()
     mag, e = np.abs(g), np.zeros((N, D))
     dx, df, bx, bf = (np.zeros((N, L, D)) for _ in range(4))
     for t in range(L - 1, -1, -1):
-        k = np.minimum(np.abs(f[:, t]), 100) + 16
+        k = far * np.minimum(np.abs(f[:, t]), 100) + 16
         g = g + dout[:, t]
         mag = mag + np.abs(dout[:, t])
         e = e + U * mag

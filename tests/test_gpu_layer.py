@@ -200,6 +200,90 @@ def test_scan_backward_nonfinite_documents(F):
     assert torch.equal(got["dinitial"], clean["dinitial"])
 
 
+# Gates far below zero.  Beside layer_ref's (|f| + 12) U, log2(e) as an fp32 is
+# 0.22 U off, so the exponent's argument is off by 1.22 |f| U at most.
+FAR = 1.25
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,L,D,low", [(1, 1, 64, 20), (2, 300, 64, 79), (3, 130, 7, 79), (1, 200, 70, 20), (2, 90, 67, 14), (1, 500, 96, 79)])
+def test_scan_closed_gates(F, N, L, D, low, dtype):
+    """A closed gate lets little through, but that little to the accuracy of
+    its type: df and dinitial are proportional to it, and the state where x is 0."""
+    t = TYPES[dtype]
+    x, f, m, h0, dout, dstate = scan_case(N, L, D, "random", True, t, 19)
+    g = gen(N + L + D)
+    shut = torch.rand((N, L, D), generator=g).cuda() < 0.5
+    shut[:, 0] |= shut[:, -1]
+    f = torch.where(shut, (-low * torch.rand((N, L, D), generator=g)).to(t).cuda(), f)
+    x = torch.where(shut & (torch.rand((N, L, D), generator=g) < 0.5).cuda(), 0, x)
+    m[:, 0] = m[:, -1] = False
+    args = np64(x), np64(f), m.cpu().numpy(), np64(h0)
+    out, state, marks = F.scan(x, f, m, h0, want_marks=True)
+    h, b, _, _ = ref.scan(*args, far=FAR)
+    ref.check(out, h, b, t, "out")
+    ref.check(state, h[:, -1], b[:, -1], torch.float32, "state")
+    blocks = range(F.SCAN_BLOCK, L, F.SCAN_BLOCK)
+    if len(blocks):
+        ref.check(marks[:, 1:], h[:, [i - 1 for i in blocks]], b[:, [i - 1 for i in blocks]], torch.float32, "marks")
+    got = F.scan_bwd(x, f, dout, dstate, m, h0, marks)
+    want = ref.scan_bwd(args[0], args[1], np64(dout), np64(dstate), args[2], args[3], far=FAR)
+    ref.check(got["dx"], *want["dx"], t, "dx")
+    ref.check(got["df"], *want["df"], t, "df")
+    ref.check(got["dinitial"], *want["dinitial"], torch.float32, "dinitial")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scan_closed_gates_against_differences(F, dtype):
+    """df of single tokens against central differences of the fp64 formula, each
+    element by itself.  A step of 1e-4 leaves s^2/6 = 2e-9 of it; with x = 0 the
+    state is a h0, so the difference's rounding is 2^-52 / 1e-4 of it; the
+    kernel's own is layer_ref's bound, at most 2^-15, and half a step of its type."""
+    t = TYPES[dtype]
+    n = 64
+    f = torch.linspace(-79, -1, n).to(t).cuda()[None, None]
+    h0, dout = normal(gen(3), 1, n, shift=2.0), normal(gen(4), 1, 1, n, dtype=t)
+    got = np64(F.scan_bwd(torch.zeros_like(f), f, dout, initial_state=h0)["df"])[0, 0]
+    loss = lambda s: ref.scan(np.zeros((1, 1, n)), np64(f) + s, None, np64(h0))[0][0, 0] * np64(dout)[0, 0]  # noqa: E731
+    d = (loss(1e-4) - loss(-1e-4)) / 2e-4
+    assert (np.abs(got - d) <= (ref.half(t) + 2.0 ** -15 + 1e-8) * np.abs(d)).all(), np.abs(got / d - 1).max()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 67])
+def test_scan_step_closed_gates(F, D, dtype):
+    t = TYPES[dtype]
+    g = gen(D)
+    N = 40
+    f = (-79 * torch.rand((N, D), generator=g)).to(t).cuda()
+    x, s = normal(g, N, D, dtype=t), normal(g, N, D)
+    x[:, ::2] = 0
+    out, nxt = F.scan_step(x, f, s, state_out=torch.empty_like(s))
+    h, b, _, _ = ref.scan(np64(x)[:, None], np64(f)[:, None], None, np64(s), far=FAR)
+    ref.check(out, h[:, 0], b[:, 0], t, "out")
+    ref.check(nxt, h[:, 0], b[:, 0], torch.float32, "state")
+
+
+@pytest.mark.parametrize("D", [24, 64, 66, 67])
+def test_scan_infinite_gates_bf16(F, D):
+    """In bf16 too f = +inf keeps the state to the bit and f = -inf replaces it,
+    backward and in a single step as well."""
+    x, f, _, h0, dout, dstate = scan_case(2, 300, D, "none", True, torch.bfloat16, 21)
+    keep = torch.full_like(f, float("inf"))
+    out, state = F.scan(x, keep, initial_state=h0)
+    assert torch.equal(state, h0) and torch.equal(out[:, 17], h0.bfloat16())
+    assert torch.equal(F.scan_step(x[:, 0], keep[:, 0], h0.clone())[1], h0)
+    out, state = F.scan(x, -keep, initial_state=h0)
+    assert torch.equal(out, x) and torch.equal(state, x[:, -1].float())
+    assert torch.equal(F.scan_step(x[:, 0], -keep[:, 0], h0.clone())[1], x[:, 0].float())
+    got = F.scan_bwd(x, -keep, dout, dstate, initial_state=h0)
+    last = (dout[:, -1].float() + dstate).bfloat16()
+    assert torch.equal(got["dx"][:, :-1], dout[:, :-1]) and torch.equal(got["dx"][:, -1], last)
+    assert (got["df"] == 0).all() and (got["dinitial"] == 0).all()
+    got = F.scan_bwd(x, keep, torch.zeros_like(dout), dstate, initial_state=h0)
+    assert torch.equal(got["dinitial"], dstate) and (got["dx"] == 0).all() and (got["df"] == 0).all()
+
+
 def test_scan_in_segments_and_steps(F):
     """Two segments with the state handed on, and single-token steps, give the
     forward of the whole within twice its bound."""
