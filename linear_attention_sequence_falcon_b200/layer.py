@@ -422,14 +422,15 @@ def residual_norm(r, weight, eps: float, y=None, scale=None, r_out=None, h=None,
     """falcon_residual_norm: the residual stream r [..., D] plus scale [D] times
     y, and that divided by its root mean square, times weight [D].  Returns
     (r_out, h); r_out may be `r` itself (the stream updated in place), and is
-    `r` where there is no y."""
+    `r` where there is no y; h may be `r` or `y`, not r_out."""
     if stream is None and r_out is None and h is None and _quick is not None:
         got = _quick.residual_norm(r, weight, eps, y, scale)
         if got is not None:
             return got
     R, D = check_residual_norm_shapes(r, weight, y, scale, r_out=r_out, h=h)
     eps = _eps(eps)
-    if h is not None and r_out is not None and h.data_ptr() == r_out.data_ptr() and R:
+    kept = r if r_out is None and y is None else r_out  # the stream that is returned, unless a new array
+    if h is not None and kept is not None and h.data_ptr() == kept.data_ptr() and R:
         raise FalconError("h and r_out are the same array")
     at = r.get_device()
     if _elsewhere(at, stream):

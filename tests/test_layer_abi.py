@@ -199,3 +199,15 @@ def test_binding_refuses_residual_norm():
     _refused(F.residual_norm_bwd, r, w, 1e-6, _t(4, 9))
     _refused(F.residual_norm_bwd, r, w, 1e-6, r, y=r, dy=same)         # without a scale dy is dr
     _refused(F.residual_norm_bwd, r, w, 1e-6, r, y=r, scale=w, dr=same, dy=same)
+
+
+def test_binding_refuses_norm_over_the_stream_it_returns():
+    """Without y the stream that residual_norm returns is r itself: h may not be
+    written over it (with an r_out of its own, or with y, it may)."""
+    import linear_attention_sequence_falcon_b200 as F
+    r, w = _t(4, 8), _t(8, dtype=torch.float32)
+    _refused(F.residual_norm, r, w, 1e-6, h=r, match="same array")
+    _refused(F.residual_norm, r, w, 1e-6, h=r.view(4, 8), match="same array")
+    _refused(F.residual_norm, r, w, 1e-6, r_out=r, h=r, match="same array")
+    for kw in (dict(r_out=_t(4, 8), h=r), dict(y=_t(4, 8), h=r), dict(h=_t(4, 8))):
+        _refused(F.residual_norm, r, w, 1e-6, **kw, match="no CPU path")  # taken
