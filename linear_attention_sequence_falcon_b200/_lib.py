@@ -32,6 +32,7 @@ EXPORTS = ("falcon_fwd", "falcon_fwd_ex", "falcon_fwd_workspace_size", "falcon_f
            "falcon_residual_norm_bwd_ws")
 
 _lib = None
+on_load = []  # called once the in-tree library is loaded: what else maps it (layer.py's short way)
 
 
 class FalconError(RuntimeError):
@@ -109,6 +110,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = argtypes, I
     _lib = lib
+    if os.path.exists(LIB_PATH) and os.path.samefile(path, LIB_PATH):
+        for call in on_load:
+            call()
     return lib
 
 

@@ -45,6 +45,19 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _replaceable(path):
+    """Refuses to build a library that this process has loaded: it would go on
+    with the old code, whatever is loaded from the new file later."""
+    try:
+        with open("/proc/self/maps") as maps:
+            loaded = any(line.rstrip("\n").removesuffix(" (deleted)").endswith(os.path.realpath(path)) for line in maps)
+    except OSError:
+        return
+    if loaded:
+        raise RuntimeError("%s is out of date, and loaded in this process: build before the first call, or in a process "
+                           "of its own" % os.path.basename(path))
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     lib = build_library(force, verbose)
     build_quick(force, verbose)
@@ -64,6 +77,7 @@ def build_quick(force: bool = False, verbose: bool = False) -> str:
         same = not os.path.isdir(BUILD)  # a copy of the tree without its _build/: the module was built elsewhere
     if not force and same and not _stale(QUICK, [src, os.path.join(INCLUDE, "falcon.h"), os.path.abspath(__file__)]):
         return QUICK
+    _replaceable(QUICK)
     os.makedirs(BUILD, exist_ok=True)
     base = os.path.dirname(torch.__file__)
     inc = [sysconfig.get_path("include"), os.path.join(base, "include"),
@@ -96,6 +110,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         same_sources = False
     if not force and same_sources and not _stale(LIB, deps + [os.path.abspath(__file__)]):
         return LIB
+    _replaceable(LIB)
     os.makedirs(BUILD, exist_ok=True)
     headers = [d for d in deps if not d.endswith(".cu")]
     objs = []

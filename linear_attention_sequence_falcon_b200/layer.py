@@ -15,9 +15,10 @@ contiguous last axis whose tokens lie evenly, such as half of a projection.
 The small calls are bound by the host (kernels of 2-3 us), so a call whose
 arrays are as they should be, on the current device, goes the short way through
 _quick (csrc/quick_layer.cpp: the same checks, allocations and call in C++, half
-the time).  It answers None for anything else, and the way below is taken: it
-refuses with words, or handles what the short way does not (another device or
-stream, arrays to write into for the norms' passes, a workspace given).
+the time), from the load of the library on.  It answers None for anything else,
+and the way below is taken: it refuses with words, or handles what the short way
+does not (another device or stream, arrays to write into for the norms' passes,
+a workspace given).
 """
 from __future__ import annotations
 
@@ -26,12 +27,23 @@ import functools
 
 import torch
 
-from ._lib import DTYPES, FalconError, _check, _shape_error, load
+from ._lib import DTYPES, FalconError, _check, _shape_error, load, on_load
 
-try:
-    from . import _quick
-except ImportError:  # not built (build.py), or for another torch: every call goes the long way
-    _quick = None
+_quick = None  # the short way, where it is built and load() has loaded the library
+
+
+def _bind_quick():
+    """Imports the short way.  It maps libfalcon.so, so not before load() does:
+    a build() in front of that would leave this process with the old kernels."""
+    global _quick
+    try:
+        from . import _quick as module
+    except ImportError:  # not built (build.py), or for another torch: every call goes the long way
+        return
+    _quick = module
+
+
+on_load.append(_bind_quick)
 
 SCAN_BLOCK = 64      # tokens between two marks of scan
 NORM_MAX_D = 16384   # the longest row of the norms
