@@ -1,6 +1,6 @@
 """Builds libfalcon.so (the C-ABI library) in-tree with nvcc for sm_100a, and
-_quick.so (csrc/quick_layer.cpp, the short way into the layer operators) with
-g++ against the torch that is installed.
+_quick.<torch>-<python>.so (csrc/quick_layer.cpp, the short way into the layer
+operators) with g++ against the torch that is installed.
 
     python -m linear_attention_sequence_falcon_b200.build [--force]
 
@@ -15,13 +15,16 @@ import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfalcon.so")
-QUICK = os.path.join(PKG, "_quick.so")
+# shares the C++ types of one torch and Python, so its name says which
+QUICK = os.path.join(PKG, "_quick.%s-%s.so" % (torch.__version__, sys.implementation.cache_tag))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -65,20 +68,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 def build_quick(force: bool = False, verbose: bool = False) -> str:
-    """_quick.so: rebuilt when its source, the ABI's header or torch changed."""
+    """The short way for this torch and Python: rebuilt when its source or the ABI's header changed."""
     import sysconfig
-    import torch
     src = os.path.join(CSRC, "quick_layer.cpp")
-    manifest = os.path.join(BUILD, "quick.txt")
-    made_for = "torch %s, python %s" % (torch.__version__, sys.version)
-    try:
-        same = open(manifest).read() == made_for
-    except OSError:
-        same = not os.path.isdir(BUILD)  # a copy of the tree without its _build/: the module was built elsewhere
-    if not force and same and not _stale(QUICK, [src, os.path.join(INCLUDE, "falcon.h"), os.path.abspath(__file__)]):
+    if not force and not _stale(QUICK, [src, os.path.join(INCLUDE, "falcon.h"), os.path.abspath(__file__)]):
         return QUICK
     _replaceable(QUICK)
-    os.makedirs(BUILD, exist_ok=True)
     base = os.path.dirname(torch.__file__)
     inc = [sysconfig.get_path("include"), os.path.join(base, "include"),
            os.path.join(base, "include", "torch", "csrc", "api", "include"),
@@ -94,8 +89,6 @@ def build_quick(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("g++ failed: " + " ".join(cmd))
     os.replace(tmp, QUICK)
-    with open(manifest, "w") as fh:
-        fh.write(made_for)
     return QUICK
 
 

@@ -24,6 +24,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
+import os
 
 import torch
 
@@ -36,10 +38,12 @@ def _bind_quick():
     """Imports the short way.  It maps libfalcon.so, so not before load() does:
     a build() in front of that would leave this process with the old kernels."""
     global _quick
-    try:
-        from . import _quick as module
-    except ImportError:  # not built (build.py), or for another torch: every call goes the long way
+    from . import build
+    if not os.path.exists(build.QUICK):  # not built, or for another torch: every call goes the long way
         return
+    spec = importlib.util.spec_from_file_location(__package__ + "._quick", build.QUICK)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
     _quick = module
 
 

@@ -27,12 +27,17 @@ def copy(tmp_path):
     return run
 
 
+def quick():
+    from linear_attention_sequence_falcon_b200 import build
+    return os.path.basename(build.QUICK)
+
+
 HEAD = """
 import os, sys
 sys.path.insert(0, os.getcwd())
 import linear_attention_sequence_falcon_b200 as F
 from linear_attention_sequence_falcon_b200 import build, layer
-mapped = lambda: {n for n in ("libfalcon.so", "_quick.so") for l in open("/proc/self/maps") if l.rstrip().endswith(os.path.join(build.PKG, n))}
+mapped = lambda: {p for p in (build.LIB, build.QUICK) for l in open("/proc/self/maps") if l.rstrip().endswith(p)}
 """
 
 
@@ -43,7 +48,7 @@ assert not mapped(), mapped()
 build.build()
 assert not mapped(), mapped()
 F.load()
-assert mapped() == {"libfalcon.so", "_quick.so"} and layer._quick is not None
+assert mapped() == {build.LIB, build.QUICK} and layer._quick is not None
 build.build()  # nothing to do
 """)
     assert r.returncode == 0, r.stderr[-2000:]
@@ -51,10 +56,10 @@ build.build()  # nothing to do
 
 def test_short_way_built_after_the_import_is_bound(copy):
     """A clean tree's first process takes the short way too."""
-    os.rename(copy.path / NAME / "_quick.so", copy.path / "_quick.so.away")
+    os.rename(copy.path / NAME / quick(), copy.path / "away")
     r = copy("""
 assert layer._quick is None
-os.rename("_quick.so.away", build.QUICK)
+os.rename("away", build.QUICK)
 F.load()
 assert layer._quick is not None
 """)
@@ -62,7 +67,7 @@ assert layer._quick is not None
 
 
 def test_build_refuses_to_replace_a_loaded_library(copy):
-    for target, source in (("libfalcon.so", "common.cuh"), ("_quick.so", "quick_layer.cpp")):
+    for target, source in (("libfalcon.so", "common.cuh"), (quick(), "quick_layer.cpp")):
         before = os.stat(copy.path / NAME / target)  # (an import changes the access time)
         r = copy("""
 F.load()
@@ -74,3 +79,27 @@ build.build()
         after = os.stat(copy.path / NAME / target)
         assert (after.st_ino, after.st_mtime_ns) == (before.st_ino, before.st_mtime_ns)
         os.utime(copy.path / NAME / "csrc" / source, (before.st_mtime - 100,) * 2)
+
+
+@pytest.mark.parametrize("objects", [True, False])
+def test_short_way_for_another_torch_is_neither_bound_nor_kept(copy, objects):
+    """A module made for another torch is not imported, and the one for this torch
+    is built beside it, also in a copy of the tree without _build/."""
+    if not objects:
+        shutil.rmtree(copy.path / "_build")
+    made = copy.path / NAME / quick()
+    code = """
+F.load()
+assert (layer._quick is not None) == %s
+def refuse(*args, **kw):
+    raise LookupError("built again")
+build.subprocess.run = refuse
+build.build_quick()
+"""
+    r = copy(code % True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    import torch
+    assert torch.__version__ in quick() and sys.implementation.cache_tag in quick()
+    made.rename(made.with_name(quick().replace(torch.__version__, "1.0")))
+    r = copy(code % False)
+    assert "LookupError: built again" in r.stderr, r.stderr[-2000:]
