@@ -3,9 +3,9 @@
 // state, their exchange inside a cluster, and the choice of the cluster's size.
 #pragma once
 
-#include <mutex>
 #include <type_traits>
 
+#include "cluster_choice.h"
 #include "common.cuh"
 #include "kernels.h"
 #include "params_layer.h"
@@ -14,7 +14,6 @@
 namespace falcon {
 namespace scan {
 
-constexpr int kMaxCluster = 16;  // beyond 8: not portable, allowed per kernel
 constexpr uint64_t kGiveUpNs = 2000000000ull;  // a wait for the cluster's maps
 
 
@@ -266,65 +265,38 @@ inline bool pair_aligned(const void *p, size_t elt, long long ld) {
 }
 
 // How many clusters of `cs` blocks of a kernel the device holds at once, from
-// the occupancy calculator, kept per (kernel, device, cs).  Also lets the
-// kernel have its dynamic shared memory on that device.
-template <typename K> int clusters_held(K kernel, int cs, int threads, size_t smem) {
-    constexpr int kDevices = 16, kKernels = 64;
-    static std::mutex guard;
-    static struct { const void *k; int held[kDevices][kMaxCluster + 1]; } kept[kKernels];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    std::lock_guard<std::mutex> lock(guard);
-    int *slot = nullptr;
-    for (auto &e : kept) {
-        if (e.k == nullptr) e.k = reinterpret_cast<const void *>(kernel);
-        if (e.k == reinterpret_cast<const void *>(kernel)) {
-            if (dev < kDevices) slot = &e.held[dev][cs];
-            break;
-        }
-    }
-    if (slot && *slot) return *slot;
-    if (smem > 0) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+// the occupancy calculator.  Also lets the kernel have its clusters and its
+// dynamic shared memory (of the largest cluster) on that device.
+template <typename K> int ask_device(K kernel, int cs, int threads, size_t smem, size_t smem_each) {
+    const int most = (int)(smem + kMaxCluster * smem_each);
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(cs * 148);
     c.blockDim = dim3(threads);
-    c.dynamicSmemBytes = smem;
+    c.dynamicSmemBytes = smem + cs * smem_each;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = cs; at.val.clusterDim.y = 1; at.val.clusterDim.z = 1;
     c.attrs = &at;
     c.numAttrs = 1;
     int held = 0;
-    if (cudaOccupancyMaxActiveClusters(&held, kernel, &c) != cudaSuccess || held < 1) {
-        cudaGetLastError();
-        held = 1;
-    }
-    if (slot) *slot = held;
-    return held;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&held, kernel, &c) == cudaSuccess)
+        return held;
+    cudaGetLastError();
+    return kNotAsked;
 }
 
-// The cluster's size: blocks walk steps = tiles/cs tiles each, in as many waves
-// as the device needs for all units' clusters.  A step takes a latency (its
-// exchange) and a share of the SM that grows with the blocks on it, a wave its
-// start: waves x (steps x (1.5 + blocks per SM) + 4.5) fits what was measured
-// over sizes 1 to 16 of six shapes; the least, the smallest size of equals.
-// Least waves x steps took 5 for the forward pass at 8x2048x768 (21.1 us; 4
-// takes 19.3); without the waves' start the backward pass at 16x1024x1024 took
-// 16 (69 us; 3 takes 39).
 // `smem_each`: shared memory for every block of the cluster, beside `smem`.
 template <typename K>
 int pick_cluster(K kernel, long long units, int tiles, int threads, size_t smem, size_t smem_each) {
-    int best = 1;
-    long long cost = 0;
-    for (int cs = 1; cs <= kMaxCluster && cs <= tiles; ++cs) {
-        const int held = clusters_held(kernel, cs, threads, smem + cs * smem_each);
-        const long long waves = (units + held - 1) / held;
-        const long long blocks = (units < held ? units : held) * cs;  // at once
-        const long long here = waves * ((tiles + cs - 1) / cs * (3 * 148 + 2 * blocks) + 9 * 148);
-        if (cs == 1 || here < cost) { best = cs; cost = here; }
-    }
-    return best;
+    static ClustersHeld kept;  // of the kernels of this type
+    int dev = -1;
+    cudaGetDevice(&dev);
+    return choose_cluster(units, tiles, [&](int cs) {
+        return kept.get(reinterpret_cast<const void *>(kernel), dev, cs,
+                        [&] { return ask_device(kernel, cs, threads, smem, smem_each); });
+    });
 }
 
 template <typename K, typename... P>
