@@ -114,6 +114,20 @@ PyObject *checked(PyObject *r) {
     return r;
 }
 
+// The library's call with Python's lock released, as ctypes makes it: a launch
+// waits where the device's queue is full, and other threads run meanwhile (the
+// one among them that the queue waits for, where a host function needs the lock).
+class Unlock {
+    PyThreadState *const state_ = PyEval_SaveThread();
+
+public:
+    ~Unlock() { PyEval_RestoreThread(state_); }
+};
+template <typename... P, typename... A> int unlocked(int (*call)(P...), A... args) {
+    const Unlock held;
+    return call(args...);
+}
+
 #define ARGUMENTS(count)                                                        \
     if (n != (count)) {                                                         \
         PyErr_SetString(PyExc_TypeError, "_quick: wrong number of arguments");  \
@@ -147,8 +161,8 @@ PyObject *scan(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!out) new_out = c.empty(shape), out = &new_out;
     if (!last && truth(a[7])) new_last = c.empty_f32({N, D}), last = &new_last;
     if (!marks && truth(a[8])) new_marks = c.empty_f32({N, blocks, D}), marks = &new_marks;
-    if (falcon_scan(c.dtype(), ptr(x), ptr(f), static_cast<const unsigned char *>(ptr(reset)), f32(init), (int)N, (int)L,
-                    (int)D, ldx, ldf, ptr(out), f32(last), f32(marks), c.stream()) != FALCON_OK)
+    if (unlocked(falcon_scan, c.dtype(), ptr(x), ptr(f), static_cast<const unsigned char *>(ptr(reset)), f32(init), (int)N,
+                 (int)L, (int)D, ldx, ldf, ptr(out), f32(last), f32(marks), c.stream()) != FALCON_OK)
         ELSEWHERE;
     return checked(tuple({object(out, a[4]), object(last, a[5]), object(marks, a[6])}));
     END_HANDLE_TH_ERRORS
@@ -182,9 +196,9 @@ PyObject *scan_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!df) new_df = c.empty(shape), df = &new_df;
     const Tensor dinitial = c.empty_f32({N, D});
     if (bytes) ws = c.empty_f32({(int64_t)(bytes + 3) / 4});
-    if (falcon_scan_bwd_ws(c.dtype(), ptr(x), ptr(f), static_cast<const unsigned char *>(ptr(reset)), f32(init), f32(marks),
-                           (int)N, (int)L, (int)D, ldx, ldf, ptr(dout), f32(dstate), ptr(dx), lddx, ptr(df), lddf,
-                           f32(&dinitial), bytes ? ws.data_ptr() : nullptr, bytes, c.stream()) != FALCON_OK)
+    if (unlocked(falcon_scan_bwd_ws, c.dtype(), ptr(x), ptr(f), static_cast<const unsigned char *>(ptr(reset)), f32(init),
+                 f32(marks), (int)N, (int)L, (int)D, ldx, ldf, ptr(dout), f32(dstate), ptr(dx), lddx, ptr(df), lddf,
+                 f32(&dinitial), bytes ? ws.data_ptr() : nullptr, bytes, c.stream()) != FALCON_OK)
         ELSEWHERE;
     return checked(tuple({object(dx, a[7]), object(df, a[8]), object(&dinitial, nullptr)}));
     END_HANDLE_TH_ERRORS
@@ -207,8 +221,8 @@ PyObject *scan_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!c.ok) ELSEWHERE;
     Tensor new_out;
     if (!out) new_out = c.empty(shape), out = &new_out;
-    if (falcon_scan_step(c.dtype(), ptr(x), ptr(f), f32(state), (int)shape[0], (int)shape[1], ldx, ldf,
-                         f32(next ? next : state), ptr(out), c.stream()) != FALCON_OK)
+    if (unlocked(falcon_scan_step, c.dtype(), ptr(x), ptr(f), f32(state), (int)shape[0], (int)shape[1], ldx, ldf,
+                 f32(next ? next : state), ptr(out), c.stream()) != FALCON_OK)
         ELSEWHERE;
     return checked(tuple({object(out, a[4]), Py_NewRef(next ? a[3] : a[2])}));
     END_HANDLE_TH_ERRORS
@@ -260,9 +274,8 @@ PyObject *norm_gate(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!c.ok) ELSEWHERE;
     Tensor new_out;
     if (!out) new_out = c.empty({g.B, g.L, g.wide}), out = &new_out;
-    if (falcon_norm_gate(c.dtype(), ptr(g.o), g.o->stride(0), g.o->stride(1), g.o->stride(2), ptr(g.gate), g.ldg,
-                         f32(g.weight), g.per_head, g.eps, (int)g.B, (int)g.H, (int)g.L, (int)g.d, ptr(out),
-                         c.stream()) != FALCON_OK)
+    if (unlocked(falcon_norm_gate, c.dtype(), ptr(g.o), g.o->stride(0), g.o->stride(1), g.o->stride(2), ptr(g.gate),
+                 g.ldg, f32(g.weight), g.per_head, g.eps, (int)g.B, (int)g.H, (int)g.L, (int)g.d, ptr(out), c.stream()) != FALCON_OK)
         ELSEWHERE;
     return checked(object(out, a[4]));
     END_HANDLE_TH_ERRORS
@@ -285,12 +298,10 @@ PyObject *norm_gate_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (g.gate) dgate = c.empty({g.B, g.L, g.wide});
     if (g.weight && truth(a[5])) dweight = c.empty_f32(g.weight->sizes());
     if (bytes) ws = c.empty_f32({(int64_t)(bytes + 3) / 4});
-    if (falcon_norm_gate_bwd_ws(c.dtype(), ptr(g.o), g.o->stride(0), g.o->stride(1), g.o->stride(2), ptr(g.gate), g.ldg,
-                                f32(g.weight), g.per_head, g.eps, (int)g.B, (int)g.H, (int)g.L, (int)g.d, ptr(dout),
-                                d_o.data_ptr(), d_o.stride(0), d_o.stride(1), d_o.stride(2),
-                                dgate.defined() ? dgate.data_ptr() : nullptr, g.wide,
-                                dweight.defined() ? f32(&dweight) : nullptr, bytes ? ws.data_ptr() : nullptr, bytes,
-                                c.stream()) != FALCON_OK)
+    if (unlocked(falcon_norm_gate_bwd_ws, c.dtype(), ptr(g.o), g.o->stride(0), g.o->stride(1), g.o->stride(2), ptr(g.gate),
+                 g.ldg, f32(g.weight), g.per_head, g.eps, (int)g.B, (int)g.H, (int)g.L, (int)g.d, ptr(dout), d_o.data_ptr(),
+                 d_o.stride(0), d_o.stride(1), d_o.stride(2), dgate.defined() ? dgate.data_ptr() : nullptr, g.wide,
+                 dweight.defined() ? f32(&dweight) : nullptr, bytes ? ws.data_ptr() : nullptr, bytes, c.stream()) != FALCON_OK)
         ELSEWHERE;
     return checked(tuple({object(&d_o, nullptr), object(&dgate, nullptr), object(&dweight, nullptr)}));
     END_HANDLE_TH_ERRORS
@@ -343,8 +354,8 @@ PyObject *residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Tensor h = c.empty(g.r->sizes());
     Tensor stream;
     if (g.y) stream = c.empty(g.r->sizes());
-    if (falcon_residual_norm(c.dtype(), ptr(g.r), ptr(g.y), f32(g.scale), f32(g.weight), g.eps, (int)g.R, (int)g.D,
-                             g.y ? stream.data_ptr() : nullptr, h.data_ptr(), c.stream()) != FALCON_OK)
+    if (unlocked(falcon_residual_norm, c.dtype(), ptr(g.r), ptr(g.y), f32(g.scale), f32(g.weight), g.eps, (int)g.R,
+                 (int)g.D, g.y ? stream.data_ptr() : nullptr, h.data_ptr(), c.stream()) != FALCON_OK)
         ELSEWHERE;
     return checked(tuple({object(&stream, g.y ? nullptr : a[0]), object(&h, nullptr)}));
     END_HANDLE_TH_ERRORS
@@ -368,10 +379,10 @@ PyObject *residual_norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (g.scale) dy = c.empty(g.r->sizes()), dscale = c.empty_f32({g.D});
     if (g.weight) dweight = c.empty_f32({g.D});
     if (bytes) ws = c.empty_f32({(int64_t)(bytes + 3) / 4});
-    if (falcon_residual_norm_bwd_ws(c.dtype(), ptr(g.r), ptr(g.y), f32(g.scale), f32(g.weight), ptr(dh), ptr(dr_out), g.eps,
-                                    (int)g.R, (int)g.D, dr.data_ptr(), g.scale ? dy.data_ptr() : nullptr,
-                                    g.scale ? f32(&dscale) : nullptr, g.weight ? f32(&dweight) : nullptr,
-                                    bytes ? ws.data_ptr() : nullptr, bytes, c.stream()) != FALCON_OK)
+    if (unlocked(falcon_residual_norm_bwd_ws, c.dtype(), ptr(g.r), ptr(g.y), f32(g.scale), f32(g.weight), ptr(dh),
+                 ptr(dr_out), g.eps, (int)g.R, (int)g.D, dr.data_ptr(), g.scale ? dy.data_ptr() : nullptr,
+                 g.scale ? f32(&dscale) : nullptr, g.weight ? f32(&dweight) : nullptr, bytes ? ws.data_ptr() : nullptr,
+                 bytes, c.stream()) != FALCON_OK)
         ELSEWHERE;
     PyObject *first = object(&dr, nullptr);
     PyObject *second = g.scale ? object(&dy, nullptr) : Py_NewRef(g.y && first ? first : Py_None);

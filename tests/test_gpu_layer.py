@@ -709,6 +709,41 @@ def test_short_and_long_way_agree(F, monkeypatch):
         F.residual_norm(x.transpose(0, 1), None, 1e-6) if x.shape[0] > 1 else F.residual_norm(x[..., ::2], None, 1e-6)
 
 
+def test_short_way_lets_other_threads_run(F):
+    """A launch releases Python's lock: another thread gets on during calls of
+    the short way, without the interpreter taking the lock from the caller."""
+    import sys
+    import threading
+    from linear_attention_sequence_falcon_b200 import layer
+    assert layer._quick is not None
+    w = torch.ones(64, device="cuda")
+    x, o, r = torch.ones(1, 1, 64, device="cuda"), torch.ones(1, 1, 1, 64, device="cuda"), torch.ones(1, 64, device="cuda")
+    out, state = torch.empty_like(x), torch.empty_like(r)
+    calls = [lambda: F.scan(x, x, None, None, out, state), lambda: F.scan_bwd(x, x, x), lambda: F.scan_step(r, r, state, None, r),
+             lambda: F.norm_gate(o, x, w, 1e-6), lambda: F.norm_gate_bwd(o, x, w, 1e-6, x),
+             lambda: F.residual_norm(r, w, 1e-6), lambda: F.residual_norm_bwd(r, w, 1e-6, r)]
+    for i, call in enumerate(calls):
+        call()
+        torch.cuda.synchronize()
+        gate, ran = threading.Lock(), []
+        gate.acquire()
+        other = threading.Thread(target=lambda: (gate.acquire(), ran.append(1)))
+        other.start()
+        before = sys.getswitchinterval()
+        sys.setswitchinterval(1000.0)
+        try:
+            gate.release()
+            turns = 0
+            while not ran and turns < 50000:
+                call()
+                turns += 1
+            got = bool(ran)
+        finally:
+            sys.setswitchinterval(before)
+        other.join(60)
+        assert got, "call %d held the lock throughout" % i
+
+
 FIRST_CALL = """
 import torch
 import linear_attention_sequence_falcon_b200 as F
