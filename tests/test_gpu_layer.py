@@ -659,6 +659,30 @@ def test_streams_side_by_side(F):
         assert all(torch.equal(p, q) for p, q in zip(wa, ga)) and all(torch.equal(p, q) for p, q in zip(wb, gb))
 
 
+def test_two_threads_at_once(F):
+    """Two threads that call at once, each on a stream of its own, give what one gives."""
+    import threading
+    args = [layer_args(2, 700, 128, torch.bfloat16, 73), layer_args(3, 333, 66, torch.float32, 79)]
+    want = [layer_calls(F, a) for a in args]
+    torch.cuda.synchronize()
+    wrong, begin = [], threading.Barrier(2)
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            begin.wait()
+            for _ in range(30):
+                got = layer_calls(F, args[i])
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(p, q) for p, q in zip(want[i], got)):
+                    wrong.append(i)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join(300)
+    assert not wrong and not any(th.is_alive() for th in threads)
+
+
 def test_two_graphs_share_nothing(F):
     """Two captured graphs, replayed side by side and with new inputs."""
     args = [layer_args(2, 260, 64, torch.bfloat16, 47), layer_args(1, 515, 130, torch.float32, 53)]
@@ -775,6 +799,160 @@ def test_first_call_is_captured(F):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_short_way_refuses_what_the_long_way_refuses(F):
+    """The checks stand in layer.py and in the short way: what the first refuses the
+    second does not take.  (Wrong arrays are larger than right ones here, or views
+    of larger ones.)"""
+    from linear_attention_sequence_falcon_b200 import layer
+    q = layer._quick
+    big = torch.zeros(1 << 16, device="cuda")
+    f32 = lambda *s: big[:int(np.prod(s))].view(s)  # noqa: E731
+    t = lambda *s: f32(*s).bfloat16()  # noqa: E731
+    x, st, marks, wide = t(2, 70, 8), f32(2, 8), f32(2, 2, 8), t(2, 70, 16)
+    strided, uneven, lying = t(2, 8, 70).transpose(1, 2), t(70, 2, 8).transpose(0, 1), t(2, 1, 8).expand(2, 70, 8)
+    rows = [t(2, 71, 8), x.float(), x.cpu(), x.half(), strided, uneven, lying, x[0]]
+    whole = rows[:4] + [wide[..., :8], strided]          # where an array has to be contiguous
+    states = [f32(3, 8), st.double(), st.cpu(), f32(2, 16)[:, :8], st.bfloat16()]
+    resets = [torch.zeros(2, 70, device="cuda"), torch.zeros(2, 71, dtype=torch.bool, device="cuda"),
+              torch.zeros(2, 70, dtype=torch.bool), torch.zeros(70, 2, dtype=torch.bool, device="cuda").t()]
+
+    def each(name, good, bad, names):
+        for place, choices in bad.items():
+            for b in choices:
+                args = list(good)
+                args[place] = b
+                assert getattr(q, name)(*args) is None, (name, names(args))
+                with pytest.raises(F.FalconError):
+                    getattr(F, name)(**names(args))
+
+    scan = lambda a: dict(zip(("x", "f", "reset", "initial_state", "out", "final_state", "marks", "want_state", "want_marks"), a))  # noqa: E731
+    each("scan", [x, x, None, None, None, None, None, True, False],
+         {0: rows[1:], 1: rows, 2: resets, 3: states, 4: whole, 5: states, 6: [f32(2, 3, 8), marks.cpu(), marks.bfloat16()]}, scan)
+    bwd = lambda a: dict(zip(("x", "f", "dout", "dstate", "reset", "initial_state", "marks", "dx", "df", "workspace"), a))  # noqa: E731
+    each("scan_bwd", [x, x, x] + [None] * 7,
+         {0: rows[1:], 1: rows, 2: whole, 3: states, 4: resets, 5: states, 6: [f32(2, 3, 8), marks.cpu()], 7: rows, 8: rows}, bwd)
+    step = lambda a: dict(zip(("x", "f", "state", "state_out", "out"), a))  # noqa: E731
+    one = t(2, 8)
+    tokens = [t(3, 8), one.float(), one.cpu(), one.half(), t(8, 2).t(), t(1, 8).expand(2, 8), t(2, 1, 8)]
+    each("scan_step", [one, one, st, None, None], {0: tokens, 1: tokens, 2: states, 3: states, 4: tokens[:4] + [t(2, 16)[:, :8]]}, step)
+    o, g, w = t(2, 3, 5, 8), t(2, 5, 24), f32(8)
+    gates = [t(2, 6, 24), g.float(), g.cpu(), t(2, 24, 5).transpose(1, 2), t(5, 2, 24).transpose(0, 1), t(2, 1, 24).expand(2, 5, 24)]
+    weights = [f32(9), f32(2, 8), w.bfloat16(), w.cpu(), f32(16)[::2], f32(3, 16)[:, :8]]
+    eps = [-1.0, float("nan")]
+    heads = [o.half(), o.cpu(), t(2, 3, 8, 5).transpose(2, 3), o[0], t(2, 3, 5, 0), t(1, 1, 1, 16385)]
+    gate = lambda a: dict(zip(("o", "gate", "weight", "eps", "out"), a))  # noqa: E731
+    each("norm_gate", [o, g, w, 1e-6, None], {0: heads, 1: gates, 2: weights, 3: eps, 4: gates[:3] + [t(2, 5, 48)[..., :24]]}, gate)
+    gbwd = lambda a: dict(zip(("o", "gate", "weight", "eps", "dout", "want_dweight"), a))  # noqa: E731
+    each("norm_gate_bwd", [o, g, w, 1e-6, g, True], {0: heads, 1: gates, 2: weights, 3: eps, 4: gates[:3] + [t(2, 5, 48)[..., :24]]}, gbwd)
+    r = t(4, 8)
+    streams = [t(5, 8), r.float(), r.cpu(), t(4, 16)[:, :8], t(8, 4).t()]
+    norm = lambda a: dict(zip(("r", "weight", "eps", "y", "scale"), a))  # noqa: E731
+    each("residual_norm", [r, w, 1e-6, r, w], {0: streams, 1: weights, 2: eps, 3: streams + [None], 4: weights}, norm)
+    nbwd = lambda a: dict(zip(("r_out", "weight", "eps", "dh", "dr_out", "y", "scale"), a))  # noqa: E731
+    each("residual_norm_bwd", [r, w, 1e-6, r, r, r, w], {0: streams, 1: weights, 2: eps, 3: streams, 4: streams, 5: streams + [None], 6: weights}, nbwd)
+    assert (big == 0).all()
+
+
+# ---------------------------------------------------------------- offsets past 31 bits
+
+FAR_ROWS = 2 ** 31 + 64  # elements
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 50, 33])
+@pytest.mark.parametrize("far", ["batch", "head", "token", "gate", "dgate"])
+def test_norm_gate_far_rows(F, far, d, dtype):
+    """Rows that lie past 31 bits from the first, in each of the arrays that have
+    strides: the places in 64-bit arithmetic, forward and backward."""
+    t = TYPES[dtype]
+    B, H, L = 2, 2, 3
+    o, gate, w, dout = gate_case(B, H, L, d, "head", True, t, 37)
+    want, b = ref.norm_gate(np64(o), np64(gate), np64(w), 1e-6)
+    wantg = ref.norm_gate_bwd(np64(o), np64(gate), np64(w), 1e-6, np64(dout))
+    D = H * d
+    room = torch.empty(FAR_ROWS + 4096, dtype=t, device="cuda")
+    strides = {"batch": (FAR_ROWS, L * d, d), "head": (L * d, FAR_ROWS, d), "token": (H * d, d, FAR_ROWS // 2)}
+    do = dgate = None
+    if far in strides:
+        place = room.as_strided((B, H, L, d), strides[far] + (1,))
+        place.copy_(o)
+        o, do = place, torch.empty_like(room).as_strided((B, H, L, d), strides[far] + (1,))
+    else:
+        ld = FAR_ROWS // (B * L - 1) // 2 * 2 + 2  # the last token's row
+        place = room.as_strided((B, L, D), (L * ld, ld, 1))
+        assert (B * L - 1) * ld >= 2 ** 31
+        if far == "gate":
+            place.copy_(gate)
+            gate = place
+        else:
+            dgate = place
+    if far != "dgate":
+        ref.check(F.norm_gate(o, gate, w, 1e-6), want, b, t, "out")
+    g = F.norm_gate_bwd(o, gate, w, 1e-6, dout, do=do, dgate=dgate)
+    ref.check(g["do"], *wantg["do"], t, "do")
+    ref.check(g["dgate"], *wantg["dgate"], t, "dgate")
+    ref.check(g["dweight"], *wantg["dweight"], torch.float32, "dweight")
+
+
+def filled(*shape, dtype=torch.bfloat16, seed=0):
+    """Standard normal numbers, made in place on the GPU."""
+    return torch.empty(shape, dtype=dtype, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(seed))
+
+
+def test_norms_of_more_than_2_31_elements(F):
+    """Arrays of more than 2^31 elements, whole: their first rows, the rows around
+    that border and the last against the fp64 forms."""
+    eps = 1e-5
+    B, H, L, d = 1, 16, 1048600, 128
+    w = filled(d, dtype=torch.float32, seed=1)
+    o, gate, dout = filled(B, L, H, d, seed=2).transpose(1, 2), filled(B, L, H * d, seed=3), filled(B, L, H * d, seed=4)
+    assert o.numel() > 2 ** 31
+    out, g = F.norm_gate(o, gate, w, eps), F.norm_gate_bwd(o, gate, w, eps, dout)
+    for part in (slice(0, 5), slice(2 ** 31 // (H * d) - 3, 2 ** 31 // (H * d) + 3), slice(L - 5, L)):
+        a = np64(o[:, :, part]), np64(gate[:, part]), np64(w), eps
+        ref.check(out[:, part], *ref.norm_gate(*a), torch.bfloat16, "out")
+        want = ref.norm_gate_bwd(*a, np64(dout[:, part]))
+        ref.check(g["do"][:, :, part], *want["do"], torch.bfloat16, "do")
+        ref.check(g["dgate"][:, part], *want["dgate"], torch.bfloat16, "dgate")
+    del o, gate, dout, out, g
+    for R, D in ((131100, 16384), (268500, 8001)):
+        w, s = filled(D, dtype=torch.float32, seed=5), filled(D, dtype=torch.float32, seed=6)
+        r, y, dh = filled(R, D, seed=7), filled(R, D, seed=8), filled(R, D, seed=9)
+        assert r.numel() > 2 ** 31
+        r_out, h = F.residual_norm(r, w, eps, y=y, scale=s)
+        g = F.residual_norm_bwd(r_out, w, eps, dh, dr_out=r, y=y, scale=s)
+        for part in (slice(0, 5), slice(2 ** 31 // D - 3, 2 ** 31 // D + 3), slice(R - 5, R)):
+            (wr, br), (wh, bh) = ref.residual_norm(np64(r[part]), np64(y[part]), np64(s), np64(w), eps)
+            ref.check(r_out[part], wr, br, torch.bfloat16, "r_out")
+            ref.check(h[part], wh, bh, torch.bfloat16, "h")
+            want = ref.residual_norm_bwd(np64(r_out[part]), np64(y[part]), np64(s), np64(w), eps, np64(dh[part]), np64(r[part]))
+            ref.check(g["dr"][part], *want["dr"], torch.bfloat16, "dr")
+            ref.check(g["dy"][part], *want["dy"], torch.bfloat16, "dy")
+        del r, y, dh, r_out, h, g
+
+
+@pytest.mark.parametrize("L,D", [(2100, 524288), (2100, 524290), (2101, 524289)])
+def test_scan_of_more_than_2_31_elements(F, L, D):
+    """Two sequences, together past 31 bits of elements, in the three ways tiles
+    come: channels from all over them against the fp64 form."""
+    N, t = 2, torch.bfloat16
+    x, f, dout = (filled(N, L, D, seed=i) for i in (1, 2, 3))
+    h0 = filled(N, D, dtype=torch.float32, seed=4)
+    assert x.numel() > 2 ** 31
+    f.add_(2.0)
+    out, state, marks = F.scan(x, f, initial_state=h0, want_marks=True)
+    g = F.scan_bwd(x, f, dout, initial_state=h0, marks=marks)
+    at = torch.tensor([0, 1, 63, 64, 131071, 262145, D - 66, D - 2, D - 1], device="cuda")
+    pick = lambda a: np64(a.index_select(-1, at))  # noqa: E731
+    h, b, _, _ = ref.scan(pick(x), pick(f), None, pick(h0))
+    ref.check(out.index_select(-1, at), h, b, t, "out")
+    ref.check(state.index_select(-1, at), h[:, -1], b[:, -1], torch.float32, "state")
+    want = ref.scan_bwd(pick(x), pick(f), pick(dout), None, None, pick(h0))
+    ref.check(g["dx"].index_select(-1, at), *want["dx"], t, "dx")
+    ref.check(g["df"].index_select(-1, at), *want["df"], t, "df")
+    ref.check(g["dinitial"].index_select(-1, at), *want["dinitial"], torch.float32, "dinitial")
 
 
 # ---------------------------------------------------------------- the operators together
