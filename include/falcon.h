@@ -458,8 +458,8 @@ int falcon_decode_carry_from_prefill_ex(falcon_variant variant, falcon_dtype dty
  *   x, f     [N,L,D] dtype, row strides x_stride and f_stride (sequence n
  *            begins at n*L*stride): values and forget gates.  f = +inf keeps
  *            the state as it is (x finite); from f = -80 downwards less than
- *            2^-114 of it is left.  Down to f = -79 a_t and 1 - a_t are formed
- *            to (1.25 |f| + 8) 2^-24 of themselves, in either type.
+ *            2^-114 of it is left.  Up to |f| = 79 a_t and 1 - a_t are formed to
+ *            (1.25 |f| + 8) 2^-24 of themselves, in either type.
  *            L is at most 2^30, N*ceil(D/32) at most 2^26, D and every row
  *            stride (of a tensor of more than one row) at most 2^21.
  *   reset    [N,L] bytes, or NULL: where non-zero, token t begins a new
