@@ -42,8 +42,11 @@ def _bind_quick():
     if not os.path.exists(build.QUICK):  # not built, or for another torch: every call goes the long way
         return
     spec = importlib.util.spec_from_file_location(__package__ + "._quick", build.QUICK)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError:  # built against something else that is gone: the same
+        return
     _quick = module
 
 

@@ -103,3 +103,9 @@ build.build_quick()
     made.rename(made.with_name(quick().replace(torch.__version__, "1.0")))
     r = copy(code % False)
     assert "LookupError: built again" in r.stderr, r.stderr[-2000:]
+
+
+def test_short_way_that_does_not_load_leaves_the_long_one(copy):
+    (copy.path / NAME / quick()).write_bytes(b"not a library")
+    r = copy("F.load(); assert layer._quick is None")
+    assert r.returncode == 0, r.stderr[-2000:]
